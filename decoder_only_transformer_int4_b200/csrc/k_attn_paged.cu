@@ -1,0 +1,959 @@
+// Attention of the newest rows of each sequence over a paged KV cache.
+//
+// Row i of the n newest of a sequence of length T sees positions t < T - n + 1 + i:
+//   o_i = sum_t p_it v_t,  p_it = exp(scale q_i.k_t) / sum_t' exp(scale q_i.k_t'),
+// query head h reading kv head h / (H / Hk).  Optionally w[g][t] += sum of p_it over the rows and the
+// heads of group g.
+//
+// Bound: HBM, every K and V row of a sequence is read once for all heads of its group and all newest
+// rows (2 T Hk hd elements).  The arithmetic stays on warp-level MMAs: the rows of a (sequence, kv head)
+// - at most 16 or 32 at a time - are the M side, sixteen cached positions a step the N side.  A group
+// of 1 to 32 rows fills no 128-row tile, so a wider tensor instruction would spend its time on padding
+// while the memory waits all the same.
+//
+// Split.  The positions of all (sequence, kv head, row tile) units are cut into tiles of 64 and laid
+// end to end; every resident CTA takes an equal run of tiles, whatever the lengths.  A run crosses
+// units: a unit that lies in one CTA is finished there, a cut one leaves (m, l, o) partials, one slot
+// for the piece that begins a CTA's run and one for the piece that ends it, which attn_join_kernel adds.
+// Nothing waits for another CTA, no counter has to be cleared, and the order of every sum is fixed.
+//
+// Inside a CTA each warp takes its own 16 positions of every tile and streams them with cp.async
+// through its own ring, so the warps meet only at a unit's end.  16 positions lie within one page (a
+// page holds a power of two of at least 16 positions), so a step needs one table entry; the entries of
+// the next 32 tiles are looked up at once, one per lane.
+//
+// Arithmetic.  16-bit caches: products of m16n8k16 with fp32 sums; the probabilities enter P V as a
+// 16-bit pair hi + lo (two MMAs), so that they carry 16 (bf16) or 22 (fp16) bits and not 8 or 11: the
+// error of the result is then the rounding of its store.  fp32 queries on a half cache enter as a pair
+// too, after an exact power-of-two scale of the row.  fp32 caches: m16n8k8 tf32 with every operand as a
+// pair of 11-bit halves, three products (hi hi, hi lo, lo hi): ~2^-21 per product.  Running maximum and
+// sum in fp32, in the exponent's base 2.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <type_traits>
+#include "ms_device.cuh"
+#include "ms_launch.cuh"
+#include "ms_paged.h"
+
+namespace ms {
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStep = 16;                  // positions a warp takes at a time
+constexpr int kTile = kStep * kWarps;      // positions of a tile
+constexpr int kRing = 64;                  // tile descriptors a warp holds (two halves of 32)
+
+struct Desc {
+  long long off;   // element offset of the 16 positions' first row in the pages, -1: no page there
+  int pos0;        // first position
+  int nvalid;      // positions of the 16 that exist
+  int b, kvh;      // sequence, kv head
+  int row0;        // first row of the row tile
+  int ends;        // bits 0, 1: this tile begins the CTA's piece, the unit; bits 2, 3: ends the piece, the unit
+};
+
+struct Kargs {
+  PagedView c;
+  const void* q;
+  void* out;
+  long long ldq, ldo;
+  const int* row_start;
+  int rows, max_rows, H, hpg, rb;   // rb: the most row tiles a (sequence, kv head) may have
+  float scale2;                     // scale * log2(e)
+  float* part;                      // [CTAs][2][R][hd] unscaled sums of cut units
+  float2* ml;                       // [CTAs][2][R] their (max, sum)
+  int* pre;                         // [batch + 1] first tile of each sequence, for the later kernels
+  float* scores;                    // [batch][Hk][hpg * max_rows][capacity], or null
+  float2* stats;                    // [batch][Hk][hpg * max_rows] final (max, sum), with scores
+  int grid;                         // CTAs of the main kernel
+};
+
+// The exponent of every probability is raised by this where P enters as fp16 pairs, so that one of
+// 2^-24 keeps its lo half; it cancels in o / l.
+template <typename KT>
+constexpr float bias_of() { return std::is_same<KT, __half>::value ? 14.f : 0.f; }
+
+template <typename KT, bool Q32, int HD, int MT>
+struct Shape {
+  static constexpr bool kF32 = sizeof(KT) == 4;
+  static constexpr int R = 16 * MT;
+  static constexpr int kRowBytes = HD * sizeof(KT);
+  static constexpr int kStageBytes = 2 * kStep * kRowBytes;      // K then V of one warp's step
+  static constexpr int kStages = kStageBytes <= 8192 ? (kStageBytes <= 4096 ? 4 : 3) : 2;
+  static constexpr int kQBytes = R * HD * ((kF32 || Q32) ? 4 : 2);   // Q32 on halves: hi and lo planes
+  static constexpr int kObufStride = HD + 8;
+  static constexpr int kObufBytes = 2 * R * kObufStride * 4;
+  static constexpr int kDescBytes = kWarps * kRing * (int)sizeof(Desc);
+  static constexpr int kSmall = R * 4 * (2 + 2 * kWarps + 2);
+  static constexpr int kFixed = kWarps * kStages * kStageBytes + kQBytes + kObufBytes + kDescBytes + kSmall;
+  static size_t smem(int batch) { return kFixed + 4 * (size_t)(batch + 1); }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// the same, or 16 zero bytes where !take (nothing is read then)
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <typename KT>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo, hi with the 11 leading significant bits (exact difference)
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+template <typename T> __device__ __forceinline__ float as_float(T x);
+template <> __device__ __forceinline__ float as_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ float as_float<__half>(__half x) { return __half2float(x); }
+template <> __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T rounded(float x);
+template <> __device__ __forceinline__ float rounded<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half rounded<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// a, b as a pair of the 16-bit type, and what the rounding left of them
+template <typename KT> struct Two;
+template <> struct Two<__half> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b, float& ra, float& rb) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    ra = a - f.x;
+    rb = b - f.y;
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <> struct Two<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b, float& ra, float& rb) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const float2 f = __bfloat1622float2(h);
+    ra = a - f.x;
+    rb = b - f.y;
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+template <typename KT>
+__device__ __forceinline__ float staged(const unsigned char* p) { return as_float<KT>(*reinterpret_cast<const KT*>(p)); }
+
+// Chunk (16 bytes) c of row r of a staged K or V step.  16-bit: the 8 rows of an ldmatrix fall on all
+// banks.  fp32 K: lanes read rows 2i, 2i + 1 at four chunks each; fp32 V: rows 2t at two chunks each.
+template <bool F32>
+__device__ __forceinline__ int swz_k(int c, int r) { return F32 ? c ^ ((r & 1) << 2) : c ^ (r & 7); }
+template <bool F32>
+__device__ __forceinline__ int swz_v(int c, int r) { return F32 ? c ^ (((r >> 1) & 3) << 1) : c ^ (r & 7); }
+
+// Row range and length of sequence b; rows n = 0 (and the flag) where they make no sense.
+__device__ __forceinline__ void seq_info(const Kargs& a, int b, int& r0, int& n, int& T, bool tell) {
+  r0 = a.row_start[b];
+  const int r1 = a.row_start[b + 1];
+  T = a.c.lens[b];
+  n = r1 - r0;
+  if (r0 < 0 || r1 > a.rows || n < 0 || n > a.max_rows || T < 0 || T > a.c.capacity()) {
+    if (tell) flag_error(a.c.status, kErrShape);
+    n = 0;
+  }
+}
+// Tiles of one unit of the sequence, and its row tiles of R rows.
+__device__ __forceinline__ int unit_tiles(int T) { return (T + kTile - 1) / kTile; }
+__device__ __forceinline__ int row_tiles(const Kargs& a, int n, int R) { return (n * a.hpg + R - 1) / R; }
+
+// o / l; a row that sees nothing gives 0, one whose every score is -inf gives NaN (0 / 0), as the formula
+__device__ __forceinline__ float finish(float o, float l, int lim) { return lim <= 0 ? 0.f : o / l; }
+
+template <typename KT, bool Q32, int HD, int MT>
+__global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
+  using S = Shape<KT, Q32, HD, MT>;
+  constexpr bool F32 = S::kF32;
+  constexpr int R = S::R, NT = HD / 8, kStages = S::kStages;
+  constexpr int kCpr = S::kRowBytes / 16;          // 16-byte chunks of a row
+  constexpr float kBias = bias_of<KT>();
+  using QT = typename std::conditional<Q32, float, KT>::type;
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* const stages = smem;
+  unsigned char* const qs = stages + kWarps * kStages * S::kStageBytes;
+  float* const obuf = reinterpret_cast<float*>(qs + S::kQBytes);
+  Desc* const descs = reinterpret_cast<Desc*>(reinterpret_cast<unsigned char*>(obuf) + S::kObufBytes);
+  float* const rowc = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(descs) + S::kDescBytes);   // score factor
+  int* const slim = reinterpret_cast<int*>(rowc + R);
+  float* const mw = reinterpret_cast<float*>(slim + R);       // [kWarps][R]
+  float* const lw = mw + kWarps * R;
+  float* const mf = lw + kWarps * R;
+  float* const lf = mf + R;
+  int* const pre = reinterpret_cast<int*>(lf + R);            // [batch + 1]
+  __shared__ int wtot[kWarps];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const int B = a.c.batch;
+  pdl_wait();
+  pdl_trigger();
+
+  // first tile of every sequence
+  {
+    int carry = 0;
+    for (int i0 = 0; i0 < B; i0 += kThreads) {
+      const int i = i0 + tid;
+      int mine = 0;
+      if (i < B) {
+        int r0, n, T;
+        seq_info(a, i, r0, n, T, blockIdx.x == 0);
+        mine = unit_tiles(T) * row_tiles(a, n, R) * a.c.Hk;
+      }
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += z;
+      }
+      __syncthreads();
+      if (lane == 31) wtot[warp] = incl;
+      __syncthreads();
+      int base = carry;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) base += wtot[w];
+        carry += wtot[w];
+      }
+      if (i < B) pre[i + 1] = base + incl;
+    }
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0)
+    for (int i = tid; i <= B; i += kThreads) a.pre[i] = pre[i];
+  const int total = pre[B];
+  const int chunk = (total + a.grid - 1) / a.grid;
+  const int f0 = min((long long)total, (long long)blockIdx.x * chunk), f1 = min(total, f0 + chunk);
+  const int niter = f1 - f0;
+  if (niter <= 0) return;
+
+  Desc* const my = descs + warp * kRing;
+  unsigned char* const mystages = stages + warp * kStages * S::kStageBytes;
+
+  // descriptors of tiles it0 .. it0 + 31, one per lane
+  auto look_up = [&](int it0) {
+    const int it = it0 + lane, f = f0 + it;
+    if (it < niter) {
+      int lo = 0, hi = B;                  // the last sequence that begins at or before f
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= f) lo = mid;
+        else hi = mid;
+      }
+      const int T = a.c.lens[lo], per = unit_tiles(T);
+      const int rt = row_tiles(a, a.row_start[lo + 1] - a.row_start[lo], R);
+      const int rem = f - pre[lo], u = rem / per, tile = rem - u * per;
+      Desc d;
+      d.b = lo;
+      d.kvh = u / rt;
+      d.row0 = (u - d.kvh * rt) * R;
+      d.pos0 = tile * kTile + warp * kStep;
+      d.ends = (tile == 0 ? 3 : it == 0 ? 1 : 0) | (tile == per - 1 ? 12 : it == niter - 1 ? 4 : 0);
+      d.nvalid = max(0, min(kStep, T - d.pos0));
+      d.off = -1;
+      if (d.nvalid > 0) {
+        const int page = a.c.table[(long long)lo * a.c.max_pages + (d.pos0 >> a.c.page_shift)];
+        if (page >= 0 && page < a.c.n_pages)
+          d.off = page * a.c.page_stride + (((long long)d.kvh << a.c.page_shift) + (d.pos0 & (a.c.page() - 1))) * HD;
+        else
+          flag_error(a.c.status, kErrShape);
+      }
+      my[it & (kRing - 1)] = d;
+    }
+    __syncwarp();
+  };
+  auto issue = [&](int it) {
+    const Desc& d = my[it & (kRing - 1)];
+    const int nv = d.nvalid;
+    if (nv > 0) {
+      const long long off = d.off;
+      const uint32_t sk = smem_u32(mystages + (it % kStages) * S::kStageBytes);
+      const uint32_t sv = sk + kStep * S::kRowBytes;
+      const char* gk = static_cast<const char*>(a.c.k);
+      const char* gv = static_cast<const char*>(a.c.v);
+      if (off >= 0) {
+        gk += off * (long long)sizeof(KT);
+        gv += off * (long long)sizeof(KT);
+      }
+      const int c = lane % kCpr, r0 = lane / kCpr;
+      constexpr int kRows = 32 / kCpr;   // rows one pass of the warp copies
+      if (off >= 0 && nv == kStep) {
+#pragma unroll
+        for (int i = 0; i < kStep / kRows; ++i) {
+          const int r = i * kRows + r0;
+          cp16(sk + r * S::kRowBytes + swz_k<F32>(c, r) * 16, gk + r * S::kRowBytes + c * 16);
+          cp16(sv + r * S::kRowBytes + swz_v<F32>(c, r) * 16, gv + r * S::kRowBytes + c * 16);
+        }
+      } else {
+        // what lies behind the sequence's end (or in no page) is read as zero: stale rows may hold anything
+#pragma unroll
+        for (int i = 0; i < kStep / kRows; ++i) {
+          const int r = i * kRows + r0;
+          const bool take = off >= 0 && r < nv;
+          const int rr = take ? r : 0;
+          cp16_or_zero(sk + r * S::kRowBytes + swz_k<F32>(c, r) * 16, gk + rr * S::kRowBytes + (take ? c * 16 : 0), take);
+          cp16_or_zero(sv + r * S::kRowBytes + swz_v<F32>(c, r) * 16, gv + rr * S::kRowBytes + (take ? c * 16 : 0), take);
+        }
+      }
+    }
+    cp_commit();
+  };
+
+  look_up(0);
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (s < niter) issue(s);
+    else cp_commit();
+  }
+
+  float m[MT][2], l[MT][2], O[MT][NT][4];
+  float fac[MT][2];
+  int lim[MT][2];
+  int seq_r0 = 0, seq_n = 0, seq_T = 0, least = 0;
+  bool begins_unit = false;
+
+  for (int it = 0; it < niter; ++it) {
+    {
+      const int nx = it + kStages - 1;
+      if (nx < niter) {
+        if ((nx & 31) == 0) look_up(nx);
+        issue(nx);
+      } else {
+        cp_commit();
+      }
+    }
+    const Desc d = my[it & (kRing - 1)];
+    const int kvh = d.kvh, tile_row = d.row0;
+
+    if (d.ends & 1) {
+      begins_unit = d.ends & 2;
+      __syncthreads();   // the previous unit's rows and sums are no longer read
+      seq_info(a, d.b, seq_r0, seq_n, seq_T, false);
+      least = seq_T - seq_n + 1;   // positions that every row of the sequence sees
+      for (int r = warp; r < R; r += kWarps) {
+        const int rr = tile_row + r, i = rr / a.hpg, h = rr - i * a.hpg;
+        const bool real = i < seq_n;
+        const QT* src = static_cast<const QT*>(a.q) + (seq_r0 + (real ? i : 0)) * a.ldq + (long long)(kvh * a.hpg + h) * HD;
+        float x[HD / 32];
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k) x[k] = real ? as_float<QT>(src[k * 32 + lane]) : 0.f;
+        float f = a.scale2;
+        if constexpr (F32) {
+#pragma unroll
+          for (int k = 0; k < HD / 32; ++k) {
+            const int e = k * 32 + lane;
+            reinterpret_cast<float*>(qs)[r * HD + swz_k<true>(e >> 2, r) * 4 + (e & 3)] = x[k];
+          }
+        } else {
+          KT* hi = reinterpret_cast<KT*>(qs);
+          float up = 1.f;
+          if constexpr (Q32) {
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k) top = fmaxf(top, fabsf(x[k]));
+            top = warp_max(top);
+            // the row's largest element to [2^13, 2^14): its half keeps 11 bits and its rest 11 more
+            if (top > 0.f && top < INFINITY) {
+              int e;
+              frexpf(top, &e);
+              e = max(-100, min(100, 14 - e));
+              up = ldexpf(1.f, e);
+              f = a.scale2 * ldexpf(1.f, -e);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < HD / 32; ++k) {
+            const int e = k * 32 + lane;
+            const int at = r * HD + (((e >> 3) ^ (r & 7)) << 3) + (e & 7);
+            const float y = x[k] * up;
+            const KT yh = rounded<KT>(y);
+            hi[at] = yh;
+            if constexpr (Q32) hi[R * HD + at] = rounded<KT>(y - as_float<KT>(yh));
+          }
+        }
+        if (lane == 0) {
+          rowc[r] = f;
+          slim[r] = real ? seq_T - seq_n + i + 1 : 0;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          m[mt][k] = -INFINITY;
+          l[mt][k] = 0.f;
+          fac[mt][k] = rowc[mt * 16 + g8 + 8 * k];
+          lim[mt][k] = slim[mt * 16 + g8 + 8 * k];
+        }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) O[mt][j][k] = 0.f;
+    }
+
+    cp_wait<kStages - 1>();
+    __syncwarp();
+
+    if (d.nvalid > 0) {
+      const unsigned char* kst = mystages + (it % kStages) * S::kStageBytes;
+      const unsigned char* vst = kst + kStep * S::kRowBytes;
+      const uint32_t ku = smem_u32(kst), vu = smem_u32(vst), qu = smem_u32(qs);
+      float sc[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[mt][j][k] = 0.f;
+
+      // S = Q K^T
+      if constexpr (!F32) {
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          uint32_t kb[4];
+          {
+            const int mi = lane >> 3, r = (lane & 7) + (mi >> 1) * 8, c = ks * 2 + (mi & 1);
+            ldsm4(kb, ku + r * S::kRowBytes + swz_k<false>(c, r) * 16);
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int r = mt * 16 + (lane & 15), c = ks * 2 + (lane >> 4);
+            const uint32_t at = qu + (r * HD + ((c ^ (r & 7)) << 3)) * 2;
+            uint32_t qa[4];
+            ldsm4(qa, at);
+            mma16<KT>(sc[mt][0], qa, kb[0], kb[1]);
+            mma16<KT>(sc[mt][1], qa, kb[2], kb[3]);
+            if constexpr (Q32) {
+              ldsm4(qa, at + R * HD * 2);
+              mma16<KT>(sc[mt][0], qa, kb[0], kb[1]);
+              mma16<KT>(sc[mt][1], qa, kb[2], kb[3]);
+            }
+          }
+        }
+      } else {
+        // k index t of a step is element 16 j + 4 t (+ 2 in the second), k index t + 4 the one after it
+#pragma unroll 2
+        for (int j = 0; j < HD / 16; ++j) {
+          const float4 q0 = *reinterpret_cast<const float4*>(qs + (g8 * HD + swz_k<true>(4 * j + t4, g8) * 4) * 4);
+          const float4 q1 = *reinterpret_cast<const float4*>(qs + ((g8 + 8) * HD + swz_k<true>(4 * j + t4, g8) * 4) * 4);
+          uint32_t ah[2][4], al[2][4];
+          split_tf32(q0.x, ah[0][0], al[0][0]);
+          split_tf32(q1.x, ah[0][1], al[0][1]);
+          split_tf32(q0.y, ah[0][2], al[0][2]);
+          split_tf32(q1.y, ah[0][3], al[0][3]);
+          split_tf32(q0.z, ah[1][0], al[1][0]);
+          split_tf32(q1.z, ah[1][1], al[1][1]);
+          split_tf32(q0.w, ah[1][2], al[1][2]);
+          split_tf32(q1.w, ah[1][3], al[1][3]);
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const int r = nt * 8 + g8;
+            const float4 k4 = *reinterpret_cast<const float4*>(kst + r * S::kRowBytes + swz_k<true>(4 * j + t4, r) * 16);
+            uint32_t bh[4], bl[4];
+            split_tf32(k4.x, bh[0], bl[0]);
+            split_tf32(k4.y, bh[1], bl[1]);
+            split_tf32(k4.z, bh[2], bl[2]);
+            split_tf32(k4.w, bh[3], bl[3]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              mma8(sc[0][nt], al[s], bh[2 * s], bh[2 * s + 1]);
+              mma8(sc[0][nt], ah[s], bl[2 * s], bl[2 * s + 1]);
+              mma8(sc[0][nt], ah[s], bh[2 * s], bh[2 * s + 1]);
+            }
+          }
+        }
+      }
+
+      // scores in base 2, masks, running maximum and sum
+      const bool masked = d.pos0 + kStep > least;   // some row does not see all 16
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float s = sc[mt][j][k] * fac[mt][k >> 1];
+            if (masked && d.pos0 + 8 * j + 2 * t4 + (k & 1) >= lim[mt][k >> 1]) s = -INFINITY;
+            sc[mt][j][k] = s;
+          }
+        if (a.scores) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int rr = tile_row + mt * 16 + g8 + 8 * k;
+            if (lim[mt][k] > 0) {   // a real row; positions behind the end fall into the capacity's last 16
+              float* dst = a.scores + (((long long)d.b * a.c.Hk + kvh) * (a.hpg * a.max_rows) + rr) * a.c.capacity() + d.pos0 + 2 * t4;
+              *reinterpret_cast<float2*>(dst) = make_float2(sc[mt][0][2 * k], sc[mt][0][2 * k + 1]);
+              *reinterpret_cast<float2*>(dst + 8) = make_float2(sc[mt][1][2 * k], sc[mt][1][2 * k + 1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float top = fmaxf(fmaxf(sc[mt][0][2 * k], sc[mt][0][2 * k + 1]), fmaxf(sc[mt][1][2 * k], sc[mt][1][2 * k + 1]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float mn = fmaxf(m[mt][k], top);
+          const float safe = mn == -INFINITY ? 0.f : mn;
+          if (__any_sync(0xffffffffu, mn > m[mt][k])) {
+            const float c = exp2f(m[mt][k] - safe);
+            l[mt][k] *= c;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              O[mt][j][2 * k] *= c;
+              O[mt][j][2 * k + 1] *= c;
+            }
+          }
+          m[mt][k] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float p = exp2f(sc[mt][j][2 * k + e] - safe + kBias);
+              sc[mt][j][2 * k + e] = p;
+              sum += p;
+            }
+          l[mt][k] += sum;
+        }
+      }
+
+      // A masked row takes nothing from a position it does not see, but 0 x inf is NaN: where such
+      // positions hold a V that is not finite, the step's P V is added element by element.
+      bool odd = false;
+      if (masked && seq_n > 1) {
+        for (int r = max(0, least - d.pos0); r < d.nvalid; ++r)
+          for (int e = lane; e < HD; e += 32) {
+            const int c = e * (int)sizeof(KT) / 16;
+            const float x = staged<KT>(vst + r * S::kRowBytes + swz_v<F32>(c, r) * 16 + e * sizeof(KT) % 16);
+            odd |= !(fabsf(x) < INFINITY);
+          }
+        odd = __any_sync(0xffffffffu, odd);
+      }
+      if (odd) {
+        for (int r = 0; r < d.nvalid; ++r)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float p[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float x0 = r & 8 ? sc[mt][1][2 * k] : sc[mt][0][2 * k];
+              const float x1 = r & 8 ? sc[mt][1][2 * k + 1] : sc[mt][0][2 * k + 1];
+              p[k] = __shfl_sync(0xffffffffu, r & 1 ? x1 : x0, (lane & ~3) | ((r & 7) >> 1));
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int e = F32 ? 32 * (j >> 2) + 4 * (2 * t4 + (k & 1)) + (j & 3) : 8 * j + 2 * t4 + (k & 1);
+                const int c = e * (int)sizeof(KT) / 16;
+                const float x = staged<KT>(vst + r * S::kRowBytes + swz_v<F32>(c, r) * 16 + e * sizeof(KT) % 16);
+                if (d.pos0 + r < lim[mt][k >> 1]) O[mt][j][k] = fmaf(p[k >> 1], x, O[mt][j][k]);
+              }
+          }
+      } else if constexpr (!F32) {
+        uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // A fragment: registers (rows g, positions 2t), (rows g + 8, 2t), (g, 8 + 2t), (g + 8, 8 + 2t)
+            const int j = i >> 1, k = i & 1;
+            float ra, rb, za, zb;
+            ph[mt][i] = Two<KT>::pack(sc[mt][j][2 * k], sc[mt][j][2 * k + 1], ra, rb);
+            pl[mt][i] = Two<KT>::pack(ra, rb, za, zb);
+          }
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+          uint32_t vb[4];
+          const int r = lane & 15, c = 2 * j + (lane >> 4);
+          ldsm4t(vb, vu + r * S::kRowBytes + swz_v<false>(c, r) * 16);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16<KT>(O[mt][2 * j], ph[mt], vb[0], vb[1]);
+            mma16<KT>(O[mt][2 * j + 1], ph[mt], vb[2], vb[3]);
+            mma16<KT>(O[mt][2 * j], pl[mt], vb[0], vb[1]);
+            mma16<KT>(O[mt][2 * j + 1], pl[mt], vb[2], vb[3]);
+          }
+        }
+      } else {
+        // k index t is position 8 nt + 2 t, t + 4 the one after it; column n of tile 4 J + jj is
+        // element 32 J + 4 n + jj, so that a lane's V loads are 16 bytes
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          uint32_t ah[4], al[4];
+          split_tf32(sc[0][nt][0], ah[0], al[0]);
+          split_tf32(sc[0][nt][2], ah[1], al[1]);
+          split_tf32(sc[0][nt][1], ah[2], al[2]);
+          split_tf32(sc[0][nt][3], ah[3], al[3]);
+          const int ra = 8 * nt + 2 * t4, rb = ra + 1;
+#pragma unroll
+          for (int J = 0; J < HD / 32; ++J) {
+            const float4 x = *reinterpret_cast<const float4*>(vst + ra * S::kRowBytes + swz_v<true>(8 * J + g8, ra) * 16);
+            const float4 y = *reinterpret_cast<const float4*>(vst + rb * S::kRowBytes + swz_v<true>(8 * J + g8, rb) * 16);
+            const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+              uint32_t xh, xl, yh, yl;
+              split_tf32(xs[jj], xh, xl);
+              split_tf32(ys[jj], yh, yl);
+              mma8(O[0][4 * J + jj], al, xh, yh);
+              mma8(O[0][4 * J + jj], ah, xl, yl);
+              mma8(O[0][4 * J + jj], ah, xh, yh);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();   // the ring's next copy goes into this stage
+
+    if (d.ends & 4) {
+      // the four warps' maxima and sums, then their weighted sums of V in two rounds
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float s = l[mt][k];
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          if (t4 == 0) {
+            mw[warp * R + mt * 16 + g8 + 8 * k] = m[mt][k];
+            lw[warp * R + mt * 16 + g8 + 8 * k] = s;
+          }
+        }
+      __syncthreads();
+      if (tid < R) {
+        float top = mw[tid];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, mw[w * R + tid]);
+        const float safe = top == -INFINITY ? 0.f : top;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += lw[w * R + tid] * exp2f(mw[w * R + tid] - safe);
+        mf[tid] = top;
+        lf[tid] = s;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int round = 0; round < 2; ++round) {
+        if ((warp & 1) == round) {
+          float* buf = obuf + (warp >> 1) * R * S::kObufStride;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int r = mt * 16 + g8 + 8 * k;
+              const float top = mf[r];
+              const float c = exp2f(m[mt][k] - (top == -INFINITY ? 0.f : top));
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int dim = F32 ? 32 * (j >> 2) + 4 * (2 * t4 + e) + (j & 3) : 8 * j + 2 * t4 + e;
+                  float* p = buf + r * S::kObufStride + dim;
+                  const float v = O[mt][j][2 * k + e] * c;
+                  *p = round ? *p + v : v;
+                }
+            }
+        }
+        __syncthreads();
+      }
+      const int real = min(R, seq_n * a.hpg - tile_row);
+      if (begins_unit && (d.ends & 8)) {
+        QT* dst = static_cast<QT*>(a.out);
+        for (int i = tid; i < real * HD; i += kThreads) {
+          const int r = i / HD, e = i - r * HD;
+          const int rr = tile_row + r, row = rr / a.hpg, h = rr - row * a.hpg;
+          const float o = obuf[r * S::kObufStride + e] + obuf[(R + r) * S::kObufStride + e];
+          dst[(seq_r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * HD + e] = rounded<QT>(finish(o, lf[r], slim[r]));
+        }
+        if (a.scores && tid < real)
+          a.stats[((long long)d.b * a.c.Hk + kvh) * (a.hpg * a.max_rows) + tile_row + tid] = make_float2(mf[tid], lf[tid]);
+      } else {
+        const long long slot = (long long)blockIdx.x * 2 + (begins_unit ? 1 : 0);
+        for (int i = tid; i < real * HD; i += kThreads) {
+          const int r = i / HD, e = i - r * HD;
+          a.part[(slot * R + r) * HD + e] = obuf[r * S::kObufStride + e] + obuf[(R + r) * S::kObufStride + e];
+        }
+        if (tid < real) a.ml[slot * R + tid] = make_float2(mf[tid], lf[tid]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// The pieces of each cut unit, added in the order of the CTAs: o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c
+// - M) l_c.  Also writes the rows of sequences that hold nothing.
+// ---------------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+
+template <typename QT>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(Kargs a, int R) {
+  __shared__ float sM[32], sL[32];
+  __shared__ float4 red[kJoinThreads];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kvh = blockIdx.x / a.rb, rt = blockIdx.x - kvh * a.rb, b = blockIdx.y, hd = a.c.hd;
+  int r0, n, T;
+  seq_info(a, b, r0, n, T, false);
+  const int row0 = rt * R, real = min(R, n * a.hpg - row0);
+  if (real <= 0) return;
+  QT* dst = static_cast<QT*>(a.out);
+  if (T == 0) {
+    for (int i = tid; i < real * hd; i += kJoinThreads) {
+      const int rr = row0 + i / hd, row = rr / a.hpg, h = rr - row * a.hpg;
+      dst[(r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * hd + i % hd] = rounded<QT>(0.f);
+    }
+    return;
+  }
+  const int per = unit_tiles(T), total = a.pre[a.c.batch], chunk = (total + a.grid - 1) / a.grid;
+  const int u0 = a.pre[b] + (kvh * row_tiles(a, n, R) + rt) * per;
+  const int c0 = u0 / chunk, c1 = (u0 + per - 1) / chunk, pieces = c1 - c0 + 1;
+  if (pieces == 1) return;
+  // piece k is the second slot of CTA c0 (it begins the unit), or the first slot of CTA c0 + k
+  auto slot = [&](int k) { return (long long)(c0 + k) * 2 + (k == 0 ? 1 : 0); };
+  for (int r = warp; r < real; r += kJoinThreads / 32) {
+    float top = -INFINITY;
+    for (int k = lane; k < pieces; k += 32) top = fmaxf(top, a.ml[slot(k) * R + r].x);
+    top = warp_max(top);
+    const float safe = top == -INFINITY ? 0.f : top;
+    float s = 0.f;
+    for (int k = lane; k < pieces; k += 32) {
+      const float2 v = a.ml[slot(k) * R + r];
+      s = fmaf(v.y, exp2f(v.x - safe), s);
+    }
+    s = warp_sum(s);
+    if (lane == 0) {
+      sM[r] = safe;
+      sL[r] = s;
+      if (a.scores) a.stats[((long long)b * a.c.Hk + kvh) * (a.hpg * a.max_rows) + row0 + r] = make_float2(top, s);
+    }
+  }
+  __syncthreads();
+  const int items = real * hd / 4;                               // four elements of a row each
+  const int parts = max(1, min(pieces, kJoinThreads / items));   // threads that share an item's pieces
+  for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
+    const int part = parts > 1 ? tid / items : 0, item = parts > 1 ? tid - part * items : i0 + tid;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (item < items && part < parts) {
+      const int r = item / (hd / 4), e = 4 * (item - r * (hd / 4));
+#pragma unroll 4
+      for (int k = part; k < pieces; k += parts) {
+        const float c = exp2f(a.ml[slot(k) * R + r].x - sM[r]);
+        const float4 x = *reinterpret_cast<const float4*>(a.part + (slot(k) * R + r) * hd + e);
+        o.x = fmaf(c, x.x, o.x);
+        o.y = fmaf(c, x.y, o.y);
+        o.z = fmaf(c, x.z, o.z);
+        o.w = fmaf(c, x.w, o.w);
+      }
+    }
+    if (parts > 1) {
+      red[tid] = o;
+      __syncthreads();
+      if (tid < items)
+        for (int p = 1; p < parts; ++p) {
+          const float4 x = red[tid + p * items];
+          o.x += x.x;
+          o.y += x.y;
+          o.z += x.z;
+          o.w += x.w;
+        }
+    }
+    if (item < items && part == 0) {
+      const int r = item / (hd / 4), e = 4 * (item - r * (hd / 4));
+      const int rr = row0 + r, row = rr / a.hpg, h = rr - row * a.hpg, lim = T - n + row + 1;
+      QT* p = dst + (r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * hd + e;
+      p[0] = rounded<QT>(finish(o.x, sL[r], lim));
+      p[1] = rounded<QT>(finish(o.y, sL[r], lim));
+      p[2] = rounded<QT>(finish(o.z, sL[r], lim));
+      p[3] = rounded<QT>(finish(o.w, sL[r], lim));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// w[b][g][t] += sum over the newest rows i and the group's heads of 2^(s - M + bias) / L, from the
+// scores that the main kernel left.  One thread owns a position, so the order of its sum is fixed.
+// ---------------------------------------------------------------------------------
+constexpr int kWeightThreads = 256;
+
+__global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(Kargs a, float* weights, long long ldw, float bias) {
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.y, b = blockIdx.z, t = blockIdx.x * kWeightThreads + threadIdx.x;
+  int r0, n, T;
+  seq_info(a, b, r0, n, T, false);
+  if (t >= T || n <= 0) return;
+  const long long unit = (long long)b * a.c.Hk + g;
+  const int rows = n * a.hpg, most = a.hpg * a.max_rows;
+  const float* s = a.scores + unit * most * a.c.capacity() + t;
+  const float2* st = a.stats + unit * most;
+  float w = 0.f;
+  // the first row that sees position t
+  const int first = max(0, t - (T - n)) * a.hpg;
+#pragma unroll 4
+  for (int r = first; r < rows; ++r) {
+    const float2 ml = st[r];
+    w += exp2f(s[(long long)r * a.c.capacity()] - ml.x + bias) / ml.y;
+  }
+  weights[unit * ldw + t] += w;
+}
+
+// Sizes of one call, the same for the workspace and for the launch.
+struct Plan {
+  int mt, R, hpg, rb, grid;
+  size_t smem, part, ml, pre, stats, scores, bytes;
+};
+
+template <typename KT, bool Q32, int HD>
+Plan plan_for(const AttnPagedArgs& a, int n_sm) {
+  Plan p;
+  p.hpg = a.H / a.c.Hk;
+  const long long rows = (long long)p.hpg * a.max_rows;
+  p.mt = sizeof(KT) == 4 || rows <= 16 ? 1 : 2;
+  p.R = 16 * p.mt;
+  p.rb = (int)((rows + p.R - 1) / p.R);
+  p.smem = p.mt == 1 ? Shape<KT, Q32, HD, 1>::smem(a.c.batch) : Shape<KT, Q32, HD, 2>::smem(a.c.batch);
+  const int fit = (int)((228 * 1024) / (p.smem + 1024));
+  const int per_sm = fit < 1 ? 1 : fit > 3 ? 3 : fit;
+  const long long tiles = (long long)a.c.batch * a.c.Hk * p.rb * ((a.c.capacity() + kTile - 1) / kTile);
+  p.grid = (int)(tiles < (long long)per_sm * n_sm ? tiles : (long long)per_sm * n_sm);
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  p.part = 0;
+  p.ml = p.part + up((size_t)p.grid * 2 * p.R * HD * 4);
+  p.pre = p.ml + up((size_t)p.grid * 2 * p.R * 8);
+  p.stats = p.pre + up(4 * (size_t)(a.c.batch + 1));
+  const size_t most = a.weights ? (size_t)a.c.batch * a.c.Hk * rows : 0;
+  p.scores = p.stats + up(most * 8);
+  p.bytes = p.scores + up(most * a.c.capacity() * 4);
+  return p;
+}
+
+template <typename KT, bool Q32, int HD>
+cudaError_t attn_go(const Launch& L, const AttnPagedArgs& a, int n_sm, void* ws) {
+  using QT = typename std::conditional<Q32, float, KT>::type;
+  const Plan p = plan_for<KT, Q32, HD>(a, n_sm);
+  char* w = static_cast<char*>(ws);
+  Kargs k;
+  k.c = a.c;
+  k.q = a.q;
+  k.out = a.out;
+  k.ldq = a.ldq;
+  k.ldo = a.ldo;
+  k.row_start = a.row_start;
+  k.rows = a.rows;
+  k.max_rows = a.max_rows;
+  k.H = a.H;
+  k.hpg = p.hpg;
+  k.rb = p.rb;
+  k.scale2 = a.scale * 1.44269504088896340736f;
+  k.part = reinterpret_cast<float*>(w + p.part);
+  k.ml = reinterpret_cast<float2*>(w + p.ml);
+  k.pre = reinterpret_cast<int*>(w + p.pre);
+  k.scores = a.weights ? reinterpret_cast<float*>(w + p.scores) : nullptr;
+  k.stats = reinterpret_cast<float2*>(w + p.stats);
+  k.grid = p.grid;
+  cudaError_t e;
+  if constexpr (sizeof(KT) == 4) {
+    e = launch_k(L, attn_paged_kernel<KT, Q32, HD, 1>, dim3(p.grid), dim3(kThreads), p.smem, k);
+  } else {
+    e = p.mt == 1 ? launch_k(L, attn_paged_kernel<KT, Q32, HD, 1>, dim3(p.grid), dim3(kThreads), p.smem, k)
+                  : launch_k(L, attn_paged_kernel<KT, Q32, HD, 2>, dim3(p.grid), dim3(kThreads), p.smem, k);
+  }
+  if (e != cudaSuccess) return e;
+  e = launch_k(L, attn_join_kernel<QT>, dim3(a.c.Hk * p.rb, a.c.batch), dim3(kJoinThreads), 0, k, p.R);
+  if (e != cudaSuccess || !a.weights) return e;
+  return launch_k(L, attn_weights_kernel, dim3((a.c.capacity() + kWeightThreads - 1) / kWeightThreads, a.c.Hk, a.c.batch),
+                  dim3(kWeightThreads), 0, k, a.weights, a.ldw, bias_of<KT>());
+}
+
+// Calls f with the kernel family's template arguments.
+template <typename F>
+auto with_types(int q_elem, int kv_elem, int hd, F&& f) {
+#define MS_CASE(KT, Q32) return hd == 64 ? f.template operator()<KT, Q32, 64>() : f.template operator()<KT, Q32, 128>()
+  if (kv_elem == kF32) MS_CASE(float, false);
+  if (kv_elem == kBf16) MS_CASE(__nv_bfloat16, false);
+  if (q_elem == kF32) MS_CASE(__half, true);
+  MS_CASE(__half, false);
+#undef MS_CASE
+}
+
+struct DoPlan {
+  const AttnPagedArgs& a;
+  int n_sm;
+  template <typename KT, bool Q32, int HD> size_t operator()() { return plan_for<KT, Q32, HD>(a, n_sm).bytes; }
+};
+struct DoLaunch {
+  const Launch& L;
+  const AttnPagedArgs& a;
+  int n_sm;
+  void* ws;
+  template <typename KT, bool Q32, int HD> cudaError_t operator()() { return attn_go<KT, Q32, HD>(L, a, n_sm, ws); }
+};
+struct DoAttrs {
+  template <typename KT, bool Q32, int HD> cudaError_t operator()() {
+    cudaError_t e = allow_smem(attn_paged_kernel<KT, Q32, HD, 1>, Shape<KT, Q32, HD, 1>::smem(kPagedMaxBatch));
+    if constexpr (sizeof(KT) == 2)
+      if (e == cudaSuccess) e = allow_smem(attn_paged_kernel<KT, Q32, HD, 2>, Shape<KT, Q32, HD, 2>::smem(kPagedMaxBatch));
+    return e;
+  }
+};
+
+}  // namespace
+
+size_t attn_paged_workspace(const AttnPagedArgs& a, int q_elem, int n_sm) {
+  return with_types(q_elem, a.c.elem, a.c.hd, DoPlan{a, n_sm});
+}
+
+cudaError_t launch_attn_paged(const Launch& L, const AttnPagedArgs& a, int q_elem, int n_sm, void* workspace) {
+  if (a.rows <= 0) return cudaSuccess;
+  return with_types(q_elem, a.c.elem, a.c.hd, DoLaunch{L, a, n_sm, workspace});
+}
+
+cudaError_t init_attrs_attn_paged() {
+  const int pairs[4][2] = {{kF32, kF32}, {kF32, kElemF16}, {kElemF16, kElemF16}, {kBf16, kBf16}};
+  for (auto& p : pairs)
+    for (int hd : {64, 128}) {
+      const cudaError_t e = with_types(p[0], p[1], hd, DoAttrs{});
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
+}
+
+}  // namespace ms

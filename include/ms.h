@@ -336,6 +336,134 @@ ms_status ms_op_lm_head_argmax_static(const float* x, int ldx, int M, int d, con
                                       const float* beta, float eps, const float* W, int V,
                                       float* logits, int32_t* argmax, void* stream);
 
+/* ---- single operations on a paged cache -------------------------------------------------
+ * For serving sequences of different lengths: the K and V rows of one layer lie in pages that a
+ * table assigns to the sequences, instead of one contiguous run per stream (ms_cache).  These calls
+ * append to such a cache, attend over it, cut it back and choose tokens after several drafted ones;
+ * the MatMuls, SkipLayerNorm and the LM head of the section above go between them.  No passage of
+ * the pages corresponds to them.
+ * All pointers inside are device pointers of the current device; every call is asynchronous on
+ * `stream`, allocates nothing, may be captured into a graph, and reads lengths, tables and row
+ * ranges on the device when it runs, so that a captured call follows them. */
+
+/* Element types of the paged operators.  F32 and F16 have the values of ms_kv_format. */
+typedef enum { MS_ELEM_F32 = 0, MS_ELEM_F16 = 1, MS_ELEM_BF16 = 2 } ms_elem;
+
+/* One layer's paged cache (a host struct, read during the call).
+ * k, v: pages [n_pages] of [n_kv_heads][page_size][head_dim] elements, page_stride elements from one
+ * page to the next (at least n_kv_heads * page_size * head_dim; more where one allocation holds
+ * several layers).  Position t of sequence b lies in row t % page_size of page
+ * table[b][t / page_size].  lens[b] is the number of positions the sequence holds, the rows of the
+ * call included.  A page may stand in several sequences' tables (a shared beginning) where no call
+ * writes into it.
+ * page_size a power of two of at least 16, head_dim 64 or 128, batch 1 .. 1024, k and v 16-byte
+ * aligned, page_stride a multiple of 16 bytes; else MS_ERR_SHAPE or MS_ERR_INVALID_ARG.
+ * status (may be NULL): a device word that calls set bits in, see ms_op_status.  A length, row range or
+ * page outside its limits is device data: the kernels check it, touch nothing outside the
+ * buffers, leave that sequence's rows out and set a bit. */
+typedef struct {
+  void* k;
+  void* v;
+  int elem; /* ms_elem */
+  int n_pages;
+  int page_size;
+  int n_kv_heads;
+  int head_dim;
+  int64_t page_stride;
+  const int32_t* table; /* [batch][max_pages] */
+  int max_pages;
+  int batch;
+  const int32_t* lens; /* [batch] */
+  uint32_t* status;
+} ms_paged_kv;
+
+/* Synchronises `stream`, reads and clears a status word of these operators (uint32, zeroed by the
+ * caller before first use) and returns MS_ERR_SHAPE (a length, row range or page out of its
+ * limits), MS_ERR_TOKEN_RANGE (a token out of range, or probabilities that sum to nothing) or
+ * MS_OK. */
+ms_status ms_op_status(uint32_t* status, void* stream);
+
+/* Rotary positions of new q and k rows and the append of k and v to the cache.
+ * The rows of the batch are packed: sequence b has rows row_start[b] .. row_start[b+1] - 1
+ * (int32 [batch + 1], not decreasing, row_start[batch] <= rows) and they are its last positions,
+ * so row r goes to position lens[b] - row_start[b+1] + r.  Rows behind row_start[batch] are left as they
+ * were.  q [rows][n_heads][head_dim], k and v [rows][n_kv_heads][head_dim] of q_elem at row strides
+ * ldq, ldk, ldv (elements: the parts of a fused QKV row are passed in place).  Pair j < rotary_dim / 2 of
+ * each q and k head, elements (j, j + rotary_dim / 2) or with interleaved (2j, 2j + 1), turns:
+ *     (a, c) -> ((a cos t - c sin t) * mscale, (a sin t + c cos t) * mscale),
+ *     t = position * inv_freq[j],  inv_freq fp64 [rotary_dim / 2];
+ * elements from rotary_dim on pass unchanged, rotary_dim = 0 appends without turning (inv_freq may
+ * then be NULL).  Scaled positions for long contexts are a matter of inv_freq and mscale; the angle
+ * is reduced in double, so far positions keep their accuracy.  The position is the cache
+ * index, or positions[r] (int32 [rows]) where not NULL: after an eviction the two differ.
+ * q_out [rows][n_heads][head_dim] of q_elem at stride ldq_out, may be q itself; q may be NULL (then q_out
+ * too): k and v alone.  k, v and q_out must not overlap the cache.  Turned in fp32, rounded once at
+ * the store.  Two rows of one call that name the same place of the same page (a page twice in the tables)
+ * are written in no fixed order.
+ * (q_elem, cache elem): (F32, F32), (F32, F16), (F16, F16), (BF16, BF16); else MS_ERR_UNSUPPORTED.
+ * rotary_dim even, 0 .. head_dim, |position| < 2^30; n_heads >= 1. */
+ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                  const void* v, int64_t ldv, int q_elem, int rows, int n_heads,
+                                  const int32_t* row_start, const int32_t* positions, const double* inv_freq,
+                                  int rotary_dim, int interleaved, float mscale, void* q_out, int64_t ldq_out,
+                                  void* stream);
+
+/* Attention of the newest rows of every sequence over the paged cache, their own positions included
+ * (append them first).  Row i of the n = row_start[b+1] - row_start[b] rows of a sequence of T =
+ * lens[b] positions sees positions t < T - n + 1 + i; query head h reads kv head
+ * h / (n_heads / n_kv_heads):
+ *     out = sum_t p_t v_t,   p = softmax_t(scale * q . k_t).
+ * A row that sees no position (T = 0, or n > T) gives 0.  What lies behind a sequence's end, or a row's last visible
+ * position, never enters, whatever the memory holds.  n <= max_rows (1 .. 64): one row is decoding,
+ * several are drafts.  q and out [rows][n_heads][head_dim] of q_elem at strides ldq, ldo; rows behind
+ * row_start[batch] are left as they were.
+ * weights (may be NULL): fp32 [batch][n_kv_heads][ldw], ldw >= max_pages * page_size: position t's entry
+ * grows by the sum of p_t over the rows and the heads of its group (for ms_op_evict_paged).
+ * The types are those of ms_op_rope_append_paged.  Scores, softmax and sums are fp32 (fp32 operands enter as pairs
+ * of 11-bit halves, probabilities as pairs of 16-bit halves); rounded once at the store.  The
+ * result of a sequence does not depend on timing, but its rounding on how the batch's work is split.
+ * workspace: ms_op_attn_paged_workspace bytes (0 for arguments that the call refuses), 256-byte
+ * aligned, holding nothing before or after; calls that may overlap on the GPU need their own.
+ * max_pages * page_size < 2^30. */
+size_t ms_op_attn_paged_workspace(const ms_paged_kv* kv, int q_elem, int n_heads, int max_rows, int with_weights);
+ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, int q_elem, int rows, int max_rows,
+                           int n_heads, float scale, const int32_t* row_start, void* out, int64_t ldo,
+                           float* weights, int64_t ldw, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Eviction by accumulated attention weight.  Of every sequence and kv head, the first `first`
+ * and the last `recent` positions are kept, and of the others those of largest weight until
+ * keep are kept (ties: the lowest index; NaN counts as largest); a sequence of at most keep positions
+ * keeps all.  The kept rows of K and V are copied in the order of their positions to positions
+ * 0, 1, .. of the pages that dst_table (int32 [batch][dst_pages], dst_pages * page_size >= keep)
+ * gives the sequence, of the same page arrays.  The pages of dst_table must not be read by
+ * this call's sequences (kv->table), except that a sequence which keeps all may keep its pages: the same entries in both.
+ * weights fp32 [batch][n_kv_heads][ldw] -> weights_out [batch][n_kv_heads][ldw_out], the kept positions'
+ * weights in the new order and 0 behind; weights_out may be weights (with ldw_out = ldw), else
+ * they must not overlap.  ldw >= max_pages * page_size, ldw_out >= keep.
+ * kept int32 [batch][n_kv_heads][keep]: the old positions, -1 behind.  lens_out int32 [batch]:
+ * min(lens, keep); not kv->lens itself.  first, recent >= 0, first + recent <= keep, keep >= 1. */
+ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t ldw, const int32_t* dst_table,
+                            int dst_pages, int keep, int first, int recent, int32_t* kept, float* weights_out,
+                            int64_t ldw_out, int32_t* lens_out, void* stream);
+
+/* Verification of drafted tokens (speculative decoding) from given random numbers.  Sequence b has n
+ * = row_start[b+1] - row_start[b] drafts, tokens int32 [rows] at row_start[b] .., 0 <= n <= max_draft (0 .. 256).
+ * target fp32 probabilities [rows + batch][vocab] at stride ld_target: row row_start[b] + b + i is
+ * the target's distribution p_i for the place of draft i, and the (n+1)-th that after all of them.
+ * draft fp32 [rows][vocab] at stride ld_draft: the distributions q_i that the drafts were drawn from, or NULL
+ * where each was certain (q_i(x) = 1).  Draft i (token x) is accepted while u_accept[row] * q_i(x) <
+ * p_i(x).  After the first refusal the next token is drawn from max(p_i - q_i, 0) (from p_i where
+ * that is zero throughout), after n acceptances from p_n: the lowest v whose cumulative sum exceeds
+ * u_sample[b] times the total.  Products and sums in double.
+ * accepted int32 [batch]; out int32 [batch][max_draft + 1]: the accepted drafts, the next token, -1 behind.
+ * Probabilities are finite and not negative (they need not sum to 1), random numbers in [0, 1).  A token outside
+ * [0, vocab) is refused, a row that sums to nothing gives the next token -1; both flag status
+ * (may be NULL), as does a row range out of its limits (nothing accepted, every token -1). */
+ms_status ms_op_verify_draft(const float* target, int64_t ld_target, const float* draft, int64_t ld_draft,
+                             const int32_t* tokens, const int32_t* row_start, int rows, int batch, int max_draft,
+                             int vocab, const float* u_accept, const float* u_sample, int32_t* accepted,
+                             int32_t* out, uint32_t* status, void* stream);
+
 /* ---- conditioner front-end ------------------------------------------------------------
  * "MuScriptor small — ONNX conversion", the conditioner graph muscriptor-small-cond.onnx:
  * audio fp32 [1, N] at 16 kHz, instrument ids [1, K] and a dataset id -> the decoder's prefix
