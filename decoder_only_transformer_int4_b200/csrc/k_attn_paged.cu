@@ -27,7 +27,9 @@
 // error of the result is then the rounding of its store.  fp32 queries on a half cache enter as a pair
 // too, after an exact power-of-two scale of the row.  fp32 caches: m16n8k8 tf32 with every operand as a
 // pair of 11-bit halves, three products (hi hi, hi lo, lo hi): ~2^-21 per product.  Running maximum and
-// sum in fp32, in the exponent's base 2.
+// sum in fp32, in the exponent's base 2.  Where the result is stored in fp32, each step's P V is summed
+// from zero and added to the running sum by a rounded addition: the tensor cores cut their sums off, which
+// over 3000 positions added up to three times the plain fp32 form's error.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -129,9 +131,12 @@ __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo, hi with the 11 leading significant bits (exact difference)
+// x = hi + lo: hi is x rounded to 11 significant bits (half away from zero), lo the exact difference, of
+// which the product uses 11 bits.  Cut off instead of rounded, hi would leave a lo of up to twice the size
+// and always x's sign: the dropped lo lo and the cut of lo would then add up over a row (measured: 2.5 times
+// the error of the result).
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
@@ -434,13 +439,19 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
       const unsigned char* kst = mystages + (it % kStages) * S::kStageBytes;
       const unsigned char* vst = kst + kStep * S::kRowBytes;
       const uint32_t ku = smem_u32(kst), vu = smem_u32(vst), qu = smem_u32(qs);
-      float sc[MT][2][4];
+      // lo: the products with a lo half, where the result is stored in fp32.  They are summed apart, since
+      // the tensor cores cut an addition's result off: fewer cuts fall on the large sum.
+      constexpr bool kApart = F32 || Q32;
+      float sc[MT][2][4], lo[kApart ? MT : 1][2][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sc[mt][j][k] = 0.f;
+          for (int k = 0; k < 4; ++k) {
+            sc[mt][j][k] = 0.f;
+            if constexpr (kApart) lo[mt][j][k] = 0.f;
+          }
 
       // S = Q K^T
       if constexpr (!F32) {
@@ -461,8 +472,8 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
             mma16<KT>(sc[mt][1], qa, kb[2], kb[3]);
             if constexpr (Q32) {
               ldsm4(qa, at + R * HD * 2);
-              mma16<KT>(sc[mt][0], qa, kb[0], kb[1]);
-              mma16<KT>(sc[mt][1], qa, kb[2], kb[3]);
+              mma16<KT>(lo[mt][0], qa, kb[0], kb[1]);
+              mma16<KT>(lo[mt][1], qa, kb[2], kb[3]);
             }
           }
         }
@@ -492,8 +503,8 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
             split_tf32(k4.w, bh[3], bl[3]);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-              mma8(sc[0][nt], al[s], bh[2 * s], bh[2 * s + 1]);
-              mma8(sc[0][nt], ah[s], bl[2 * s], bl[2 * s + 1]);
+              mma8(lo[0][nt], al[s], bh[2 * s], bh[2 * s + 1]);
+              mma8(lo[0][nt], ah[s], bl[2 * s], bl[2 * s + 1]);
               mma8(sc[0][nt], ah[s], bh[2 * s], bh[2 * s + 1]);
             }
           }
@@ -508,7 +519,9 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float s = sc[mt][j][k] * fac[mt][k >> 1];
+            float s = sc[mt][j][k];
+            if constexpr (kApart) s += lo[mt][j][k];
+            s *= fac[mt][k >> 1];
             if (masked && d.pos0 + 8 * j + 2 * t4 + (k & 1) >= lim[mt][k >> 1]) s = -INFINITY;
             sc[mt][j][k] = s;
           }
@@ -605,10 +618,23 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
           ldsm4t(vb, vu + r * S::kRowBytes + swz_v<false>(c, r) * 16);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            mma16<KT>(O[mt][2 * j], ph[mt], vb[0], vb[1]);
-            mma16<KT>(O[mt][2 * j + 1], ph[mt], vb[2], vb[3]);
-            mma16<KT>(O[mt][2 * j], pl[mt], vb[0], vb[1]);
-            mma16<KT>(O[mt][2 * j + 1], pl[mt], vb[2], vb[3]);
+            if constexpr (Q32) {
+              float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16<KT>(d0, pl[mt], vb[0], vb[1]);
+              mma16<KT>(d1, pl[mt], vb[2], vb[3]);
+              mma16<KT>(d0, ph[mt], vb[0], vb[1]);
+              mma16<KT>(d1, ph[mt], vb[2], vb[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                O[mt][2 * j][k] += d0[k];
+                O[mt][2 * j + 1][k] += d1[k];
+              }
+            } else {
+              mma16<KT>(O[mt][2 * j], ph[mt], vb[0], vb[1]);
+              mma16<KT>(O[mt][2 * j + 1], ph[mt], vb[2], vb[3]);
+              mma16<KT>(O[mt][2 * j], pl[mt], vb[0], vb[1]);
+              mma16<KT>(O[mt][2 * j + 1], pl[mt], vb[2], vb[3]);
+            }
           }
         }
       } else {
@@ -632,9 +658,12 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
               uint32_t xh, xl, yh, yl;
               split_tf32(xs[jj], xh, xl);
               split_tf32(ys[jj], yh, yl);
-              mma8(O[0][4 * J + jj], al, xh, yh);
-              mma8(O[0][4 * J + jj], ah, xl, yl);
-              mma8(O[0][4 * J + jj], ah, xh, yh);
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma8(d, al, xh, yh);
+              mma8(d, ah, xl, yl);
+              mma8(d, ah, xh, yh);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) O[0][4 * J + jj][k] += d[k];
             }
           }
         }
