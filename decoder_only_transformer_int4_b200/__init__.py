@@ -1,6 +1,8 @@
 """Python binding of libms_b200.so, the MuScriptor KV-cached INT4 decoder step on B200.
 
 Argument marshalling only: every step of the decoder runs in the library's CUDA kernels.
+The calls go through ctypes, those of the paged-cache operators, which are short enough for
+that to show, through a small extension module (csrc/py_paged.cpp).
 PyTorch is used for device memory and streams (tensors are passed by data_ptr(), the
 stream is torch's current stream).  Importing this module loads the compiled library
 and raises ImportError if it has not been built (python
@@ -24,6 +26,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "ms.h")
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python decoder_only_transformer_int4_b200/build.py`")
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _paged  # noqa: E402  (the paged operators' calls; refers to the library just loaded)
 
 MS_OK, MS_ERR_INVALID_ARG, MS_ERR_SHAPE, MS_ERR_CACHE_FULL, MS_ERR_TOKEN_RANGE = 0, 1, 2, 3, 4
 MS_ERR_OOM, MS_ERR_CUDA, MS_ERR_TIMEOUT, MS_ERR_UNSUPPORTED = 5, 6, 7, 8
@@ -278,87 +281,28 @@ def lm_head_argmax_static(x: torch.Tensor, W: torch.Tensor, gamma: Optional[torc
 _ELEMS = {torch.float32: MS_ELEM_F32, torch.float16: MS_ELEM_F16, torch.bfloat16: MS_ELEM_BF16}
 
 
-def _elem(t: torch.Tensor, name: str) -> int:
-    e = _ELEMS.get(t.dtype)
-    if e is None:
-        raise ValueError(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
-    return e
-
-
-def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
-    """Address of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _packed_rows(t: torch.Tensor, name: str, heads: int, dim: int, dtype: torch.dtype, device: torch.device) -> Tuple[int, int]:
-    """(address, row stride) of packed rows [rows, heads, dim]; a row's elements lie together."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name}: expected {dtype} [rows, {heads}, {dim}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    row, head, one = t.stride()
-    if one != 1 or (head != dim and heads > 1):
-        raise ValueError(f"{name}: the elements of a row must lie together")
-    return t.data_ptr(), row if t.shape[0] > 1 else heads * dim
-
-
-def _matrix(t: torch.Tensor, name: str, cols: int, device: torch.device) -> Tuple[int, int]:
-    """(address, row stride) of a float32 matrix with `cols` columns."""
-    if t.dim() != 2 or t.shape[1] != cols or t.dtype != torch.float32 or t.device != device or (t.stride(1) != 1 and cols > 1):
-        raise ValueError(f"{name}: expected float32 [rows, {cols}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
-
-
-def _op(device: torch.device, name: str, *args):
-    """Runs an entry point with `device` current, on its current stream."""
-    if device.index == torch.cuda.current_device():
-        status = getattr(_lib, name)(*args, torch.cuda.current_stream().cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            status = getattr(_lib, name)(*args, torch.cuda.current_stream().cuda_stream)
-    if status != MS_OK:
-        _check(status, name)
-
-
-def _status_word(status: Optional[torch.Tensor], device: torch.device) -> Optional[int]:
-    return None if status is None else _flat(status, "status", torch.int32, (1,), device)
-
-
 def op_status(status: torch.Tensor):
     """Synchronises the current stream of the word's device; raises MsError if an operator flagged device data
     it could not use (ms_op_status), and clears the word."""
-    _op(status.device, "ms_op_status", _flat(status, "status", torch.int32, (1,), status.device))
+    if status.dtype != torch.int32 or status.numel() != 1:
+        raise ValueError("status: expected one int32")
+    with torch.cuda.device(status.device):
+        _check(_lib.ms_op_status(_ptr(status), _stream()), "ms_op_status")
 
 
 class PagedKV:
     """One layer's paged cache (ms_paged_kv): K and V pages [n_pages, kv_heads, page_size, head_dim] (the
     first dimension may be strided), table int32 [batch, max_pages], lens int32 [batch] with the rows of
     the next call included; status (optional): int32 [1], zeroed, collects errors in device data (op_status).
-    Holds the tensors; writes to them in place are seen by later calls."""
+    Holds the tensors; writes to them in place are seen by later calls.  The attributes are only read: other
+    tensors need another PagedKV."""
 
-    __slots__ = ("k", "v", "table", "lens", "status", "device", "n_kv_heads", "head_dim", "capacity", "batch", "_s", "_at")
+    __slots__ = ("k", "v", "table", "lens", "status", "_h", "n_kv_heads", "head_dim", "capacity", "batch")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                  status: Optional[torch.Tensor] = None):
-        dev = k.device
-        if dev.type != "cuda":
-            raise ValueError("expected CUDA tensors")
-        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or v.device != dev:
-            raise ValueError("k and v: expected the same pages [n_pages, kv_heads, page_size, head_dim]")
-        n, hk, page, hd = k.shape
-        st = k.stride()
-        if st[3] != 1 or (st[2] != hd and page > 1) or (st[1] != page * hd and hk > 1):
-            raise ValueError("k and v: the elements of a page must lie together")
-        if table.dim() != 2:
-            raise ValueError("table: expected [batch, max_pages]")
-        batch, most = table.shape
-        self.k, self.v, self.table, self.lens, self.status, self.device = k, v, table, lens, status, dev
-        self.n_kv_heads, self.head_dim, self.capacity, self.batch = hk, hd, most * page, batch
-        self._s = PagedKVStruct(k.data_ptr(), v.data_ptr(), _elem(k, "k"), n, page, hk, hd,
-                                st[0] if n > 1 else hk * page * hd, _flat(table, "table", torch.int32, (batch, most), dev),
-                                most, batch, _flat(lens, "lens", torch.int32, (batch,), dev), _status_word(status, dev))
-        self._at = ctypes.addressof(self._s)
+        self._h, self.n_kv_heads, self.head_dim, self.capacity, self.batch = _paged.kv(k, v, table, lens, status)
+        self.k, self.v, self.table, self.lens, self.status = k, v, table, lens, status
 
 
 def rope_append_paged(kv: PagedKV, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
@@ -368,40 +312,15 @@ def rope_append_paged(kv: PagedKV, q: Optional[torch.Tensor], k: torch.Tensor, v
     no turning) and appends k and v to the cache (ms_op_rope_append_paged).  q [rows, heads, dim], k and v
     [rows, kv_heads, dim] may be slices of fused rows; row_start int32 [batch + 1]; positions int32 [rows] where they
     are not the cache indices.  Returns the turned q (out if given, which may be q), None for q None."""
-    dev = kv.device
-    rows = k.shape[0]
-    kp, ldk = _packed_rows(k, "k", kv.n_kv_heads, kv.head_dim, k.dtype, dev)
-    vp, ldv = _packed_rows(v, "v", kv.n_kv_heads, kv.head_dim, k.dtype, dev)
-    qp = ldq = op = ldo = heads = 0
-    if q is not None:
-        heads = q.shape[1] if q.dim() == 3 else 0
-        qp, ldq = _packed_rows(q, "q", heads, kv.head_dim, k.dtype, dev)
-        if out is None:
-            out = torch.empty((rows, heads, kv.head_dim), dtype=q.dtype, device=dev)
-        op, ldo = _packed_rows(out, "out", heads, kv.head_dim, k.dtype, dev)
-        if q.shape[0] != rows or out.shape[0] != rows:
-            raise ValueError("q, k, v and out: expected the same number of rows")
-    elif out is not None:
-        raise ValueError("out: goes with q")
-    if v.shape[0] != rows:
-        raise ValueError("q, k, v and out: expected the same number of rows")
-    pairs = 0 if inv_freq is None else inv_freq.shape[0]
-    _op(dev, "ms_op_rope_append_paged", kv._at, qp or None, ldq, kp, ldk, vp, ldv, _elem(k, "k"), rows, heads,
-        _flat(row_start, "row_start", torch.int32, (kv.batch + 1,), dev),
-        None if positions is None else _flat(positions, "positions", torch.int32, (rows,), dev),
-        _flat(inv_freq, "inv_freq", torch.float64, (pairs,), dev) if pairs else None, 2 * pairs, 1 if interleaved else 0,
-        mscale, op or None, ldo)
-    return out
+    r = _paged.rope(kv._h, q, k, v, row_start, inv_freq, interleaved, mscale, positions, out)
+    if r[0]:
+        _check(r[0], "ms_op_rope_append_paged")
+    return r[1] if q is not None else None
 
 
 def attn_paged_workspace(kv: PagedKV, q_dtype: torch.dtype, heads: int, max_rows: int, weights: bool = False) -> int:
     """Bytes of workspace that attn_paged needs for these sizes (ms_op_attn_paged_workspace)."""
-    if kv.device.index == torch.cuda.current_device():
-        n = _lib.ms_op_attn_paged_workspace(kv._at, _ELEMS.get(q_dtype, -1), heads, max_rows, 1 if weights else 0)
-    else:
-        with torch.cuda.device(kv.device):
-            n = _lib.ms_op_attn_paged_workspace(kv._at, _ELEMS.get(q_dtype, -1), heads, max_rows, 1 if weights else 0)
-    return int(n)
+    return _paged.attn_workspace(kv._h, _ELEMS.get(q_dtype, -1), heads, max_rows, weights)
 
 
 def attn_paged(kv: PagedKV, q: torch.Tensor, row_start: torch.Tensor, max_rows: int, scale: Optional[float] = None,
@@ -410,81 +329,35 @@ def attn_paged(kv: PagedKV, q: torch.Tensor, row_start: torch.Tensor, max_rows: 
     """Attention of the newest rows q [rows, heads, dim] (at most max_rows of a sequence) over the paged cache
     (ms_op_attn_paged); scale defaults to dim ** -0.5.  weights fp32 [batch, kv_heads, >= capacity] grows by each
     position's probabilities.  workspace: uint8, attn_paged_workspace bytes; one is allocated where None."""
-    dev = kv.device
-    heads = q.shape[1] if q.dim() == 3 else 0
-    qp, ldq = _packed_rows(q, "q", heads, kv.head_dim, q.dtype, dev)
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    op, ldo = _packed_rows(out, "out", heads, kv.head_dim, q.dtype, dev)
-    if out.shape[0] != q.shape[0]:
-        raise ValueError("q and out: expected the same number of rows")
-    wp, ldw = None, 0
-    if weights is not None:
-        ldw = weights.shape[-1]
-        wp = _flat(weights, "weights", torch.float32, (kv.batch, kv.n_kv_heads, ldw), dev)
-    if workspace is None:
-        workspace = torch.empty((max(1, attn_paged_workspace(kv, q.dtype, heads, max_rows, weights is not None)),),
-                                dtype=torch.uint8, device=dev)
-    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected contiguous uint8 on {dev}")
-    _op(dev, "ms_op_attn_paged", kv._at, qp, ldq, _elem(q, "q"), q.shape[0], max_rows, heads,
-        kv.head_dim ** -0.5 if scale is None else scale, _flat(row_start, "row_start", torch.int32, (kv.batch + 1,), dev),
-        op, ldo, wp, ldw, workspace.data_ptr(), workspace.numel())
-    return out
+    r = _paged.attn(kv._h, q, row_start, max_rows, scale, weights, out, workspace)
+    if r[0]:
+        _check(r[0], "ms_op_attn_paged")
+    return r[1]
 
 
 def evict_paged(kv: PagedKV, weights: torch.Tensor, dst_table: torch.Tensor, keep: int, first: int = 0, recent: int = 0,
-                weights_out: Optional[torch.Tensor] = None):
+                weights_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Cuts every sequence and kv head back to keep positions: the first, the recent ones and the heaviest others,
     copied in order into the pages of dst_table int32 [batch, pages] (ms_op_evict_paged).  weights fp32 [batch,
     kv_heads, >= capacity].  Returns (kept int32 [batch, kv_heads, keep], weights in the new order (weights_out, which may be
     weights), lens int32 [batch])."""
-    dev = kv.device
-    ldw = weights.shape[-1]
-    wp = _flat(weights, "weights", torch.float32, (kv.batch, kv.n_kv_heads, ldw), dev)
-    if dst_table.dim() != 2:
-        raise ValueError("dst_table: expected [batch, pages]")
-    pages = dst_table.shape[1]
-    if weights_out is None:
-        weights_out = torch.empty_like(weights)
-    ldwo = weights_out.shape[-1]
-    kept = torch.empty((kv.batch, kv.n_kv_heads, max(0, keep)), dtype=torch.int32, device=dev)
-    lens = torch.empty((kv.batch,), dtype=torch.int32, device=dev)
-    _op(dev, "ms_op_evict_paged", kv._at, wp, ldw, _flat(dst_table, "dst_table", torch.int32, (kv.batch, pages), dev), pages,
-        keep, first, recent, kept.data_ptr(),
-        _flat(weights_out, "weights_out", torch.float32, (kv.batch, kv.n_kv_heads, ldwo), dev), ldwo, lens.data_ptr())
-    return kept, weights_out, lens
+    r = _paged.evict(kv._h, weights, dst_table, keep, first, recent, weights_out)
+    if r[0]:
+        _check(r[0], "ms_op_evict_paged")
+    return r[1:]
 
 
 def verify_draft(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: torch.Tensor, row_start: torch.Tensor,
-                 max_draft: int, u_accept: torch.Tensor, u_sample: torch.Tensor, status: Optional[torch.Tensor] = None):
+                 max_draft: int, u_accept: torch.Tensor, u_sample: torch.Tensor,
+                 status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Accepts or refuses drafted tokens and draws the next one (ms_op_verify_draft).  target fp32 [rows + batch, vocab],
     draft fp32 [rows, vocab] or None for certain drafts, tokens int32 [rows], row_start int32 [batch + 1], u_accept
     fp32 [rows], u_sample fp32 [batch].  Returns (accepted int32 [batch], tokens int32 [batch, max_draft + 1]: the accepted
     drafts, the next token, -1 behind)."""
-    dev = target.device
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors")
-    rows, batch = tokens.shape[0], u_sample.shape[0]
-    vocab = target.shape[-1]
-    tp, ldt = _matrix(target, "target", vocab, dev)
-    if target.shape[0] != rows + batch:
-        raise ValueError("target: expected a row for every draft and one more for every sequence")
-    dp, ldd = None, 0
-    if draft is not None:
-        dp, ldd = _matrix(draft, "draft", vocab, dev)
-        if draft.shape[0] != rows:
-            raise ValueError("draft: expected a row for every draft")
-    accepted = torch.empty((batch,), dtype=torch.int32, device=dev)
-    out = torch.empty((batch, max(0, max_draft) + 1), dtype=torch.int32, device=dev)
-    if batch == 0:
-        return accepted, out
-    _op(dev, "ms_op_verify_draft", tp, ldt, dp, ldd, _flat(tokens, "tokens", torch.int32, (rows,), dev) or None,
-        _flat(row_start, "row_start", torch.int32, (batch + 1,), dev), rows, batch, max_draft, vocab,
-        _flat(u_accept, "u_accept", torch.float32, (rows,), dev) or None,
-        _flat(u_sample, "u_sample", torch.float32, (batch,), dev), accepted.data_ptr(), out.data_ptr(),
-        _status_word(status, dev))
-    return accepted, out
+    r = _paged.verify(target, draft, tokens, row_start, max_draft, u_accept, u_sample, status)
+    if r[0]:
+        _check(r[0], "ms_op_verify_draft")
+    return r[1:]
 
 
 # ---- model and cache -------------------------------------------------------------------

@@ -1,4 +1,5 @@
-"""Build the CUDA library libms_b200.so in-tree with nvcc for sm_100a.
+"""Build the CUDA library libms_b200.so in-tree with nvcc for sm_100a, and the Python extension _paged.so
+(host code against torch's headers) that calls it.
 
 Usage: python decoder_only_transformer_int4_b200/build.py [--force] [--verbose-ptxas]
 (run by path: importing the package itself loads the library this script builds)
@@ -7,10 +8,12 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -18,6 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libms_b200.so")
 SOURCES = ["k_elementwise.cu", "k_gemv.cu", "k_gemm_f16.cu", "k_w4a8.cu", "k_gemm_i8.cu", "k_attn.cu", "k_attn_tc.cu", "k_decode_persistent.cu", "k_cond.cu", "ms_runtime.cu",
            "ms_noalloc.cu", "k_paged.cu", "k_attn_paged.cu", "k_verify.cu", "ms_paged.cu"]
+EXT = os.path.join(HERE, "_paged" + sysconfig.get_config_var("EXT_SUFFIX"))
+EXT_SOURCE = "py_paged.cpp"
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]
@@ -54,6 +59,22 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_extension() -> None:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    lib = os.path.join(torch, "lib")
+    tmp = EXT + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, EXT_SOURCE), "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+           "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{EXT_SOURCE} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, ptxas_v: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     todo = [s for s in SOURCES if force or ptxas_v or
@@ -68,6 +89,8 @@ def build(force: bool = False, ptxas_v: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if force or _stale(EXT, EXT_SOURCE):
+        _build_extension()
     return LIB
 
 
