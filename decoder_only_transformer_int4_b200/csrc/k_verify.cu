@@ -10,10 +10,14 @@
 // ~1e-15 of the total, where fp32 sums would move the border between neighbouring tokens by more
 // than many of their probabilities.
 //
-// Bound: HBM for large vocabularies (one row of p and one of q per sequence), launch latency for
-// small ones.  A cluster of CTAs shares a sequence's row: each warp sums a contiguous run, the
-// runs' sums are exchanged over distributed shared memory, and the one warp whose run holds the
-// border walks it again (it is in L1 or L2 by then).
+// Bound: latency.  One row of p and one of q per sequence is 2 to 25 MB at 32 to 64 sequences, 0.4 to 4 us
+// of HBM; the chain row range -> token -> p(x), q(x) -> row -> border is about five dependent loads long.
+// A cluster of CTAs shares a sequence's row.  Each warp sums a contiguous run; every CTA writes its runs'
+// sums into all CTAs of the cluster, so that one cluster barrier is the only wait; the warp whose run
+// holds the border then narrows it 32 times at a step (each lane sums a contiguous piece, it is in L1 or L2
+// by then) instead of walking it.  Walked 32 values a step, the border cost more than all else: 18.6 us for
+// 64 sequences of 32003 tokens and 26.9 us for 32 of 100003, against 8.0 us and
+// 10.7 us (4.8 us for one sequence of 1393 tokens; half the threads, or half the CTAs: 10% to 30% more).
 #include <cooperative_groups.h>
 #include <math.h>
 #include "ms_device.cuh"
@@ -23,11 +27,20 @@
 namespace ms {
 
 namespace {
-constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32, kVerMaxCluster = 8;
+constexpr int kVerThreads = 512, kVerWarps = kVerThreads / 32, kVerMaxCluster = 8;
+constexpr int kVerRuns = kVerMaxCluster * kVerWarps, kPerLane = kVerRuns / 32;
 
 __device__ __forceinline__ double warp_sum_d(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_scan_d(double v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double z = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += z;
+  }
   return v;
 }
 }  // namespace
@@ -35,10 +48,11 @@ __device__ __forceinline__ double warp_sum_d(double v) {
 __global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a, unsigned* status) {
   namespace cg = cooperative_groups;
   __shared__ int first_refused;
-  __shared__ double sums[2][kVerWarps];   // this CTA's runs: of the wanted weights, of p
+  __shared__ double sums[kVerRuns];   // of the runs of the whole cluster
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cluster.barrier_arrive();   // waited for before the first write into another CTA: all have begun then
   pdl_wait();
   pdl_trigger();
   const int r0 = a.row_start[b];
@@ -70,72 +84,61 @@ __global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a,
       }
       for (int j = tid; j <= a.max_draft; j += kVerThreads) out[j] = -1;
     }
-    return;   // the whole cluster: none waits at its barrier
+    cluster.barrier_wait();
+    return;   // the whole cluster: none waits at its second barrier
   }
   const bool refused = taken < n;
   const float* p = a.target + (long long)(r0 + b + taken) * a.ldt;
   const float* q = refused && a.draft ? a.draft + (long long)(r0 + taken) * a.ldd : nullptr;
-  const int banned = refused && !a.draft ? a.tokens[r0 + taken] : -1;
-  auto rest = [&](int v, float pv, float qv) -> double {
-    if (!refused) return pv;
-    if (!q) return v == banned ? 0.0 : (double)pv;
-    return fmax((double)pv - (double)qv, 0.0);
-  };
+  int banned = refused && !a.draft ? a.tokens[r0 + taken] : -1;
 
   // this warp's run of the row
   const int runs = C * kVerWarps, len = (a.V + runs - 1) / runs;
   const int run = rank * kVerWarps + warp;
   const int v0 = min((long long)a.V, (long long)run * len), v1 = min(a.V, v0 + len);
-  double s = 0.0, sp = 0.0;
   constexpr int U = 8;
-  int v = v0 + lane;
-  for (; v + 32 * (U - 1) < v1; v += 32 * U) {
-    float pv[U], qv[U];
+  double x[kPerLane], mine, incl, total;
+  cluster.barrier_wait();
+  while (true) {
+    double s[4] = {0.0, 0.0, 0.0, 0.0};   // apart, so that additions do not wait for one another
+    if (q) {
+      for (int v = v0 + lane; v < v1; v += 32 * U) {
+        float pv[U], qv[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      pv[k] = p[v + 32 * k];
-      qv[k] = q ? q[v + 32 * k] : 0.f;
+        for (int k = 0; k < U; ++k) {
+          const bool in = v + 32 * k < v1;
+          pv[k] = in ? p[v + 32 * k] : 0.f;
+          qv[k] = in ? q[v + 32 * k] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) s[k & 3] += fmax((double)pv[k] - (double)qv[k], 0.0);
+      }
+    } else {
+      for (int v = v0 + lane; v < v1; v += 64 * U) {
+        float pv[2 * U];
+#pragma unroll
+        for (int k = 0; k < 2 * U; ++k) pv[k] = v + 32 * k < v1 ? p[v + 32 * k] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 2 * U; ++k) s[k & 3] += v + 32 * k == banned ? 0.f : pv[k];
+      }
     }
+    const double all = warp_sum_d((s[0] + s[1]) + (s[2] + s[3]));
+    if (lane < C) cluster.map_shared_rank(sums, lane)[run] = all;
+    cluster.sync();
+    mine = 0.0;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      s += rest(v + 32 * k, pv[k], qv[k]);
-      sp += pv[k];
+    for (int k = 0; k < kPerLane; ++k) {
+      const int r = kPerLane * lane + k;
+      x[k] = r < runs ? sums[r] : 0.0;
+      mine += x[k];
     }
+    incl = warp_scan_d(mine, lane);
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    if (total > 0.0 || !(q || banned >= 0)) break;
+    q = nullptr;   // the whole cluster: p itself
+    banned = -1;
+    cluster.sync();   // the sums have been read
   }
-  for (; v < v1; v += 32) {
-    const float pv = p[v];
-    s += rest(v, pv, q ? q[v] : 0.f);
-    sp += pv;
-  }
-  s = warp_sum_d(s);
-  sp = warp_sum_d(sp);
-  if (lane == 0) {
-    sums[0][warp] = s;
-    sums[1][warp] = sp;
-  }
-  cluster.sync();
-  // every warp reads all runs' sums (at most 64: two a lane) and finds the run with the border
-  double x[2][2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int r = 2 * lane + k;
-    x[0][k] = x[1][k] = 0.0;
-    if (r < runs) {
-      const double* other = cluster.map_shared_rank(&sums[0][0], r / kVerWarps);
-      x[0][k] = other[r % kVerWarps];
-      x[1][k] = other[kVerWarps + r % kVerWarps];
-    }
-  }
-  cluster.sync();   // no CTA leaves while another reads its sums
-  const bool fall_back = !(warp_sum_d(x[0][0] + x[0][1]) > 0.0);
-  const double a0 = fall_back ? x[1][0] : x[0][0], a1 = fall_back ? x[1][1] : x[0][1];
-  double incl = a0 + a1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double z = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += z;
-  }
-  const double total = __shfl_sync(0xffffffffu, incl, 31);
   if (rank == 0 && warp == 0) {
     for (int j = lane; j <= a.max_draft; j += 32)
       if (j != taken) out[j] = j < taken ? a.tokens[r0 + j] : -1;
@@ -149,50 +152,57 @@ __global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a,
     return;
   }
   const double goal = (double)a.u_sample[b] * total;
-  double before0 = __shfl_up_sync(0xffffffffu, incl, 1);
-  if (lane == 0) before0 = 0.0;
-  const double mid = before0 + a0;
+  double at = __shfl_up_sync(0xffffffffu, incl, 1);
+  if (lane == 0) at = 0.0;
   // the last run that begins at or below the goal and has any weight
   int r = -1;
-  double at = 0.0;
-  if (a0 > 0.0 && before0 <= goal) {
-    r = 2 * lane;
-    at = before0;
-  }
-  if (a1 > 0.0 && mid <= goal) {
-    r = 2 * lane + 1;
-    at = mid;
+  double begin = 0.0;
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    if (x[k] > 0.0 && at <= goal) {
+      r = kPerLane * lane + k;
+      begin = at;
+    }
+    at += x[k];
   }
   const unsigned has = __ballot_sync(0xffffffffu, r >= 0);
   const int from = has ? 31 - __clz(has) : 0;
   r = __shfl_sync(0xffffffffu, r, from);
-  at = __shfl_sync(0xffffffffu, at, from);
+  at = __shfl_sync(0xffffffffu, begin, from);
   if (r != run) return;
-  // this warp holds the border: walk its run in order
-  int found = -1, last = -1;
-  for (int w0 = v0; w0 < v1 && found < 0; w0 += 32) {
-    const int w = w0 + lane;
-    double y = 0.0;
-    if (w < v1) y = fall_back ? (double)p[w] : rest(w, p[w], q ? q[w] : 0.f);
-    double c = y;
+  // This warp holds the border.  [lo, hi) is narrowed to the piece of the first lane whose sum passes the
+  // goal (the last with any weight, if the goal fell behind the run by rounding) until it is one value.
+  int lo = v0, hi = v1;
+  while (true) {
+    const int step = (hi - lo + 31) / 32;
+    const int w0 = min((long long)hi, lo + (long long)lane * step), w1 = min(hi, w0 + step);
+    double part[2] = {0.0, 0.0};
+    for (int w = w0; w < w1; w += U) {
+      float pv[U], qv[U];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double z = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += z;
+      for (int k = 0; k < U; ++k) {
+        pv[k] = w + k < w1 ? p[w + k] : 0.f;
+        qv[k] = q && w + k < w1 ? q[w + k] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) part[k & 1] += w + k == banned ? 0.0 : fmax((double)pv[k] - (double)qv[k], 0.0);
     }
-    const unsigned over = __ballot_sync(0xffffffffu, y > 0.0 && at + c > goal);
+    const double y = part[0] + part[1], c = at + warp_scan_d(y, lane);
+    const unsigned over = __ballot_sync(0xffffffffu, y > 0.0 && c > goal);
     const unsigned some = __ballot_sync(0xffffffffu, y > 0.0);
-    if (over) found = w0 + __ffs(over) - 1;
-    if (some) last = w0 + 31 - __clz(some);
-    at += __shfl_sync(0xffffffffu, c, 31);
+    const int pick = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
+    at = __shfl_sync(0xffffffffu, c - y, pick);
+    lo = __shfl_sync(0xffffffffu, w0, pick);
+    hi = __shfl_sync(0xffffffffu, w1, pick);
+    if (step == 1) break;
   }
-  if (lane == 0) out[taken] = found >= 0 ? found : last;   // last: the goal fell behind the run by rounding
+  if (lane == 0) out[taken] = lo;
 }
 
 cudaError_t launch_verify_draft(const Launch& L, const VerifyArgs& a) {
-  // a CTA for each 4096 tokens of the row, up to a portable cluster
+  // a CTA for each 8192 tokens of the row (16 a thread: one or two rounds of loads), up to a portable cluster
   int C = 1;
-  while (C < kVerMaxCluster && C * 4096 < a.V) C *= 2;
+  while (C < kVerMaxCluster && C * 8192 < a.V) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.batch * C);
   cfg.blockDim = dim3(kVerThreads);
