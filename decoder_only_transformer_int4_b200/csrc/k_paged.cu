@@ -1,5 +1,6 @@
 // Rotary positions with the append into a paged cache, and eviction from it by accumulated
 // attention weight.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -250,185 +251,222 @@ cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_e
 // ---------------------------------------------------------------------------------
 // Eviction.  Per (sequence, kv head) of length T > keep: the first `first` and last `recent`
 // positions stay, and of those between the keep - first - recent of largest weight (ties: the
-// lowest index; a NaN counts as largest).  Two kernels:
+// lowest index; a NaN counts as largest).
 //
-// evict_select_kernel, one CTA per (sequence, kv head): a radix select over the weights' ordered
-// 32-bit keys (four 8-bit digits; equal digits of a warp are counted together, so that the few
-// distinct leading digits of like-sized weights do not serialise on one counter) gives the key of
-// the last one kept and how many of its equals stay; then one ordered pass writes the kept indexes
-// and their weights by rank.  The weights may be compacted in place: a rank never exceeds its
-// position, and a chunk is read before any of it is written.
+// A cluster of CTAs shares a (sequence, kv head).  Each warp takes a contiguous run of the weights and
+// holds them in shared memory (up to 20 a lane; what is longer is read again from L2 in each pass).  A radix select over
+// the weights' ordered 32-bit keys (four 8-bit digits, the histograms added over distributed shared
+// memory; equal digits of a warp are counted together, so that the few distinct leading digits of
+// like-sized weights do not serialise on one counter) gives the key of the last one kept and how many of
+// its equals stay.  Then the kept positions get their ranks, in order, from the warps' counts, and the
+// cluster moves the kept weights and the rows of K and V, 16 bytes a thread, by rank: equal shares
+// for the CTAs wherever the kept ones lie.
 //
-// evict_move_kernel copies the kept rows of K and V into the sequence's new pages, 16 bytes a
-// thread, in the order of their positions.  Bound: HBM, 2 x kept rows read and written.
+// In place, weights are moved in blocks of ranks that the whole cluster reads before it writes any: a rank
+// never exceeds its position, so that a block's writes fall on positions that no later block reads.
+//
+// Bound: HBM, 2 x kept rows read and written (10.7 and 20.8 us at 64 x 4 x 512 rows of 128 bytes and
+// 4 x 8 x 4099 of 256); the select is latency, ~1 us a digit.  One CTA per (sequence, kv head) with a second
+// kernel for the rows took 26.9 and 78.4 us, of that the select 14 and 56; this takes 20.2 and 42.0 us (rows
+// 9 and 20, a digit 0.6 and, with the cluster's barrier and the sum of its histograms, 2).
 // ---------------------------------------------------------------------------------
 namespace {
-constexpr int kSelThreads = 1024;
-constexpr int kMoveThreads = 256;
+constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32, kEvMaxCluster = 8;
+constexpr int kEvHeld = 20;   // weights a thread holds in shared memory
+constexpr int kEvRuns = kEvWarps * kEvMaxCluster;
 
+// Keys in the weights' order, all of them between those of a place without a position and of one that stays
+// in any case.  -0 counts as 0, a NaN as more than +inf.
+constexpr unsigned kKeyNone = 0, kKeyStays = 0xffffffffu;
 __device__ __forceinline__ unsigned weight_key(float w) {
-  unsigned u = w != w ? 0x7fffffffu : __float_as_uint(w + 0.0f);   // -0 counts as 0
+  const unsigned u = w != w ? 0x7f800001u : __float_as_uint(w + 0.0f);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 }  // namespace
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
-  __shared__ unsigned hist[256];
-  __shared__ unsigned pick[2];          // digit chosen, how many of its keys are still wanted
-  __shared__ unsigned wsum[32];
+__global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a, int row_shift) {
+  namespace cg = cooperative_groups;
+  __shared__ __align__(16) unsigned hist[4][256];
+  __shared__ __align__(16) unsigned total[256];
+  __shared__ int picked[4][2];        // of each pass: the digit, how many of its keys are still wanted
+  __shared__ unsigned held[kEvHeld][kEvThreads];
+  __shared__ int count[2][kEvRuns];   // of every warp of the cluster: kept for sure, equal to the last key
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = cluster.num_blocks(), rank = cluster.block_rank();
+  const int unit = blockIdx.x / C, b = unit / a.c.Hk, g = unit - b * a.c.Hk;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cluster.barrier_arrive();   // all CTAs have begun before one writes into another
+  for (int i = tid; i < 4 * 256; i += kEvThreads) (&hist[0][0])[i] = 0;
   pdl_wait();
   pdl_trigger();
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long row = (long long)b * a.c.Hk + g;
-  const float* w = a.weights + row * a.ldw;
-  float* wo = a.weights_out + row * a.ldwo;
-  int* kept = a.kept + row * a.keep;
+  const float* w = a.weights + (long long)unit * a.ldw;
+  float* wo = a.weights_out + (long long)unit * a.ldwo;
+  int* kept = a.kept + (long long)unit * a.keep;
   int T = a.c.lens[b];
-  if (T < 0 || T > a.c.capacity() || T > a.ldw) {
+  if (T < 0 || T > a.c.capacity()) {
     if (tid == 0) flag_error(a.c.status, kErrShape);
     T = 0;
   }
   const bool cut = T > a.keep;
-  const int lo = cut ? a.first : 0, hi = cut ? T - a.recent : 0;   // candidates [lo, hi)
-  const unsigned want = cut ? a.keep - a.first - a.recent : 0;
-  unsigned key = 0xffffffffu, equal = 0;   // keys above `key` stay, and the first `equal` of its equals
-  if (want) {
-    unsigned prefix = 0, left = want;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int i0 = lo; i0 < hi; i0 += kSelThreads) {
-        const int i = i0 + tid;
-        unsigned d = 256;
-        if (i < hi) {
-          const unsigned u = weight_key(w[i]);
-          if (shift == 24 || (u >> (shift + 8)) == prefix) d = (u >> shift) & 255;
+  const int n = min(T, a.keep);
+  const int lo = a.first, hi = T - a.recent;   // where cut: candidates [lo, hi)
+  auto weight = [&](int i) { return i < T ? w[i] : 0.f; };
+  auto key_of = [&](int i, float x) { return i >= T ? kKeyNone : !cut || i < lo || i >= hi ? kKeyStays : weight_key(x); };
+
+  // this warp's run: kn rows of 32 positions, lane by lane
+  const int runs = C * kEvWarps, run = rank * kEvWarps + warp;
+  const int kn = (T + 32 * runs - 1) / (32 * runs);
+  const int i0 = run * kn * 32 + lane;   // below 2 (T + 32 runs) < 2^31
+  for (int k0 = 0; k0 < min(kn, kEvHeld); k0 += 4) {
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = weight(i0 + 32 * (k0 + k));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) held[k0 + k][tid] = key_of(i0 + 32 * (k0 + k), x[k]);   // read by this thread alone
+  }
+  auto each = [&](auto&& f) {
+#pragma unroll 4
+    for (int k = 0; k < min(kn, kEvHeld); ++k) f(i0 + 32 * k, held[k][tid]);
+#pragma unroll 1
+    for (int k = kEvHeld; k < kn; ++k) f(i0 + 32 * k, key_of(i0 + 32 * k, weight(i0 + 32 * k)));
+  };
+  auto sync_all = [&] {   // the cluster's threads; what they wrote is seen
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+  };
+  __syncthreads();   // the histograms are zero
+  cluster.barrier_wait();
+
+  unsigned key = kKeyStays;
+  int equal = n;   // keys above `key` stay, and the first `equal` of its equals
+  if (cut) {       // the keep largest; those that stay in any case are among them
+    unsigned prefix = 0;
+    int left = n;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      if (pass == 0) {
+        each([&](int, unsigned u) {
+          const unsigned same = __match_any_sync(0xffffffffu, u >> 24);
+          if (lane == __ffs(same) - 1) atomicAdd(&hist[0][u >> 24], __popc(same));
+        });
+      } else {
+        each([&](int, unsigned u) {
+          if ((u >> (shift + 8)) == prefix) atomicAdd(&hist[pass][(u >> shift) & 255], 1u);
+        });
+      }
+      const unsigned* bins = hist[pass];
+      if (C > 1) {
+        cluster.sync();
+        if (tid < 256) {
+          unsigned sum = 0;
+#pragma unroll
+          for (int r = 0; r < kEvMaxCluster; ++r)
+            if (r < C) sum += *cluster.map_shared_rank(&hist[pass][tid], r);
+          total[tid] = sum;
         }
-        const unsigned same = __match_any_sync(0xffffffffu, d);
-        if (d < 256 && lane == __ffs(same) - 1) atomicAdd(&hist[d], __popc(same));
+        bins = total;
       }
       __syncthreads();
       if (warp == 0) {
-        // bins from the largest digit down: lane l holds bins 255 - 8l .. 248 - 8l
-        unsigned c[8], sum = 0;
+        // lane l holds bins 8l .. 8l + 7; from the largest digit down
+        const uint4 y = reinterpret_cast<const uint4*>(bins)[2 * lane], z = reinterpret_cast<const uint4*>(bins)[2 * lane + 1];
+        const int c[8] = {(int)z.w, (int)z.z, (int)z.y, (int)z.x, (int)y.w, (int)y.z, (int)y.y, (int)y.x};
+        int sum = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum += c[k] = hist[255 - 8 * lane - k];
-        unsigned before = sum;
+        for (int k = 0; k < 8; ++k) sum += c[k];
+        int before = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const unsigned v = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += v;
+          const int v = __shfl_down_sync(0xffffffffu, before, o);
+          if (lane + o < 32) before += v;
         }
         before -= sum;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          if (before < left && left <= before + c[k]) {
-            pick[0] = 255 - 8 * lane - k;
-            pick[1] = left - before;
+          if (before < left && left <= before + c[k]) {   // T > keep: one bin has it
+            picked[pass][0] = 8 * lane + 7 - k;
+            picked[pass][1] = left - before;
           }
           before += c[k];
         }
       }
       __syncthreads();
-      prefix = (prefix << 8) | pick[0];
-      left = pick[1];
-      __syncthreads();
+      prefix = (prefix << 8) | (unsigned)picked[pass][0];
+      left = picked[pass][1];
     }
     key = prefix;
     equal = left;
   }
-  // ranks in the order of the positions, four consecutive positions a thread; counts of sure ones
-  // in the low half of a word, of equals in the high half (a chunk has 4096 positions)
-  unsigned sure0 = 0, eq0 = 0;
-  for (int i0 = 0; i0 < T; i0 += 4 * kSelThreads) {
-    float v[4];
-    unsigned mine = 0, flags = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + 4 * tid + k;
-      v[k] = i < T ? w[i] : 0.f;
-      if (i < T) {
-        const unsigned u = weight_key(v[k]);
-        const bool inside = cut && i >= lo && i < hi;
-        if (!inside || (want && u > key)) {
-          mine += 1u;
-          flags |= 1u << k;
-        } else if (want && u == key) {
-          mine += 1u << 16;
-          flags |= 16u << k;
-        }
-      }
-    }
-    unsigned incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    __syncthreads();
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    unsigned base = 0, all = 0;
-    {
-      const unsigned x = wsum[lane];
-      unsigned y = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-      }
-      base = __shfl_sync(0xffffffffu, y - x, warp);
-      all = __shfl_sync(0xffffffffu, y, 31);
-    }
-    base += incl - mine;
-    unsigned sure = sure0 + (base & 0xffffu), eq = eq0 + (base >> 16);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool s = flags & (1u << k), e = flags & (16u << k);
-      if (s || (e && eq < equal)) {
-        const unsigned r = sure + min(eq, equal);
-        kept[r] = i0 + 4 * tid + k;
-        wo[r] = v[k];
-      }
-      sure += s;
-      eq += e;
-    }
-    sure0 += all & 0xffffu;
-    eq0 += all >> 16;
-  }
-  __syncthreads();
-  const int n = min(T, a.keep);
-  for (int i = n + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
-  for (long long i = n + tid; i < a.ldwo; i += kSelThreads) wo[i] = 0.f;
-  if (g == 0 && tid == 0) a.lens_out[b] = n;
-}
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, int row_shift) {
-  pdl_wait();
-  pdl_trigger();
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int per = kMoveThreads >> row_shift;            // rows a pass (1 << row_shift chunks of 16 bytes each)
-  const int c = threadIdx.x & ((1 << row_shift) - 1);
-  const int* kept = a.kept + ((long long)b * a.c.Hk + g) * a.keep;
+  // ranks in the order of the positions
+  int ns = 0, ne = 0;
+  each([&](int, unsigned u) {
+    ns += __popc(__ballot_sync(0xffffffffu, u > key));
+    ne += __popc(__ballot_sync(0xffffffffu, u == key));
+  });
+  if (lane < C) {
+    int* to = cluster.map_shared_rank(&count[0][0], lane);
+    to[run] = ns;
+    to[kEvRuns + run] = ne;
+  }
+  sync_all();
+  int rs = 0, re = 0;
+#pragma unroll
+  for (int k = 0; k < kEvRuns / 32; ++k) {
+    const int r = 32 * k + lane;
+    if (r < run) {
+      rs += count[0][r];
+      re += count[1][r];
+    }
+  }
+  rs = __reduce_add_sync(0xffffffffu, rs);
+  re = __reduce_add_sync(0xffffffffu, re);
+  const unsigned below = (1u << lane) - 1;
+  each([&](int i, unsigned u) {
+    const bool s = u > key, e = u == key;
+    const unsigned bs = __ballot_sync(0xffffffffu, s), be = __ballot_sync(0xffffffffu, e);
+    const int nth = re + __popc(be & below);
+    if (s || (e && nth < equal)) kept[rs + __popc(bs & below) + min(nth, equal)] = i;
+    rs += __popc(bs);
+    re += __popc(be);
+  });
+  sync_all();   // kept is whole (and read past L1: other SMs wrote it)
+
+  // weights
+  const bool in_place = wo == w;
+  for (int j0 = 0; j0 < n; j0 += C * kEvThreads) {
+    const int j = j0 + rank * kEvThreads + tid;
+    const float x = j < n ? w[__ldcg(kept + j)] : 0.f;
+    if (in_place) sync_all();
+    if (j < n) wo[j] = x;
+  }
+  for (int j = n + rank * kEvThreads + tid; j < a.keep; j += C * kEvThreads) kept[j] = -1;
+  for (long long j = n + rank * kEvThreads + tid; j < a.ldwo; j += C * kEvThreads) wo[j] = 0.f;
+  if (g == 0 && rank == 0 && tid == 0) a.lens_out[b] = n;
+
+  // rows
+  const int per = kEvThreads >> row_shift;            // rows a pass (1 << row_shift chunks of 16 bytes each)
+  const int c = tid & ((1 << row_shift) - 1);
   const int mask = a.c.page() - 1;
   const uint4* ks = static_cast<const uint4*>(a.c.k);
   const uint4* vs = static_cast<const uint4*>(a.c.v);
   uint4* kd = static_cast<uint4*>(a.c.k);
   uint4* vd = static_cast<uint4*>(a.c.v);
   const long long page16 = a.c.page_stride * (a.c.elem == kF32 ? 4 : 2) / 16;
+  const int* from_table = a.c.table + (long long)b * a.c.max_pages;
+  const int* to_table = a.dst_table + (long long)b * a.dst_pages;
   constexpr int U = 4;
-  const int j0 = blockIdx.x * per * U + (threadIdx.x >> row_shift);
-  long long src[U], dst[U];
-  uint4 xk[U], xv[U];
+  for (int j0 = rank * per * U + (tid >> row_shift); j0 < n; j0 += C * per * U) {
+    long long src[U], dst[U];
+    uint4 xk[U], xv[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int j = j0 + u * per;
-    src[u] = -1;
-    if (j < a.keep) {
-      const int i = kept[j];
-      if (i >= 0) {
-        const int sp = a.c.table[(long long)b * a.c.max_pages + (i >> a.c.page_shift)];
-        const int dp = a.dst_table[(long long)b * a.dst_pages + (j >> a.c.page_shift)];
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * per;
+      src[u] = -1;
+      if (j < n) {
+        const int i = __ldcg(kept + j);
+        const int sp = from_table[i >> a.c.page_shift], dp = to_table[j >> a.c.page_shift];
         if (sp < 0 || sp >= a.c.n_pages || dp < 0 || dp >= a.c.n_pages) {
           flag_error(a.c.status, kErrShape);
         } else {
@@ -437,29 +475,29 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, i
         }
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (src[u] >= 0) {
+        xk[u] = ks[src[u]];
+        xv[u] = vs[src[u]];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (src[u] >= 0) {
+        kd[dst[u]] = xk[u];
+        vd[dst[u]] = xv[u];
+      }
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (src[u] >= 0) {
-      xk[u] = ks[src[u]];
-      xv[u] = vs[src[u]];
-    }
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (src[u] >= 0) {
-      kd[dst[u]] = xk[u];
-      vd[dst[u]] = xv[u];
-    }
 }
 
 cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a) {
-  cudaError_t e = launch_k(L, evict_select_kernel, dim3(a.c.Hk, a.c.batch), dim3(kSelThreads), 0, a);
-  if (e != cudaSuccess) return e;
   const int chunks = a.c.hd * (a.c.elem == kF32 ? 4 : 2) / 16;   // 8, 16 or 32
   const int shift = chunks == 8 ? 3 : chunks == 16 ? 4 : 5;
-  const int rows = (kMoveThreads >> shift) * 4;
-  return launch_k(L, evict_move_kernel, dim3((a.keep + rows - 1) / rows, a.c.Hk, a.c.batch), dim3(kMoveThreads), 0, a,
-                  shift);
+  const long long units = (long long)a.c.Hk * a.c.batch;
+  // more CTAs a unit while two a SM are not reached and each warp has 64 positions
+  int C = 1;
+  while (C < kEvMaxCluster && units * C < 2 * 148 && a.c.capacity() > C * 2 * kEvThreads) C *= 2;
+  return launch_cluster(L, evict_paged_kernel, C, dim3((unsigned)(units * C)), dim3(kEvThreads), 0, a, shift);
 }
 
 }  // namespace ms

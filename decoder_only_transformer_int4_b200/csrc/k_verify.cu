@@ -203,20 +203,7 @@ cudaError_t launch_verify_draft(const Launch& L, const VerifyArgs& a) {
   // a CTA for each 8192 tokens of the row (16 a thread: one or two rounds of loads), up to a portable cluster
   int C = 1;
   while (C < kVerMaxCluster && C * 8192 < a.V) C *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.batch * C);
-  cfg.blockDim = dim3(kVerThreads);
-  cfg.stream = L.stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)C, 1, 1};
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = L.pdl ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_draft_kernel, a, L.status);
-  if (e == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
-  return e;
+  return launch_cluster(L, verify_draft_kernel, C, dim3(a.batch * C), dim3(kVerThreads), 0, a, L.status);
 }
 
 }  // namespace ms

@@ -28,6 +28,29 @@ inline cudaError_t launch_k(const Launch& L, void (*kernel)(KArgs...), dim3 grid
   return e;
 }
 
+// The same for a grid of thread-block clusters of C CTAs (C <= 8).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster(const Launch& L, void (*kernel)(KArgs...), int C, dim3 grid, dim3 block, size_t smem,
+                                  Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = L.pdl ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
+  return e;
+}
+
 // Largest dynamic shared memory a CTA may use on sm_100 (227 KiB).
 constexpr size_t kMaxDynSmem = 227 * 1024;
 
