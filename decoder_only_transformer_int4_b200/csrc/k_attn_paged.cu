@@ -47,13 +47,14 @@ constexpr int kStep = 16;                  // positions a warp takes at a time
 constexpr int kTile = kStep * kWarps;      // positions of a tile
 constexpr int kRing = 64;                  // tile descriptors a warp holds (two halves of 32)
 
-struct Desc {
-  long long off;   // element offset of the 16 positions' first row in the pages, -1: no page there
-  int pos0;        // first position
-  int nvalid;      // positions of the 16 that exist
-  int b, kvh;      // sequence, kv head
-  int row0;        // first row of the row tile
-  int ends;        // bits 0, 1: this tile begins the CTA's piece, the unit; bits 2, 3: ends the piece, the unit
+struct __align__(16) Desc {
+  long long off;         // element offset of the 16 positions' first row in the pages, -1: no page there
+  int pos0;              // first position
+  short nvalid;          // positions of the 16 that exist
+  short ends;            // bits 0, 1: this tile begins the CTA's piece, the unit; bits 2, 3: ends the piece, the unit
+  int b, kvh;            // sequence, kv head
+  int row0;              // first row of the row tile
+  int unused;
 };
 
 struct Kargs {
@@ -83,10 +84,10 @@ struct Shape {
   static constexpr int R = 16 * MT;
   static constexpr int kRowBytes = HD * sizeof(KT);
   static constexpr int kStageBytes = 2 * kStep * kRowBytes;      // K then V of one warp's step
-  static constexpr int kStages = kStageBytes <= 8192 ? (kStageBytes <= 4096 ? 4 : 3) : 2;
+  static constexpr int kStages = kStageBytes <= 4096 ? 3 : 2;
   static constexpr int kQBytes = R * HD * ((kF32 || Q32) ? 4 : 2);   // Q32 on halves: hi and lo planes
   static constexpr int kObufStride = HD + 8;
-  static constexpr int kObufBytes = 2 * R * kObufStride * 4;
+  static constexpr int kObufBytes = R * kObufStride * 4;
   static constexpr int kDescBytes = kWarps * kRing * (int)sizeof(Desc);
   static constexpr int kSmall = R * 4 * (2 + 2 * kWarps + 2);
   static constexpr int kFixed = kWarps * kStages * kStageBytes + kQBytes + kObufBytes + kDescBytes + kSmall;
@@ -104,6 +105,12 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// 2^x to 2 ulp; results below the smallest normal number are 0
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
           const float mn = fmaxf(m[mt][k], top);
           const float safe = mn == -INFINITY ? 0.f : mn;
           if (__any_sync(0xffffffffu, mn > m[mt][k])) {
-            const float c = exp2f(m[mt][k] - safe);
+            const float c = ex2(m[mt][k] - safe);
             l[mt][k] *= c;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float p = exp2f(sc[mt][j][2 * k + e] - safe + kBias);
+              const float p = ex2(sc[mt][j][2 * k + e] - safe + kBias);
               sc[mt][j][2 * k + e] = p;
               sum += p;
             }
@@ -672,7 +679,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     __syncwarp();   // the ring's next copy goes into this stage
 
     if (d.ends & 4) {
-      // the four warps' maxima and sums, then their weighted sums of V in two rounds
+      // the four warps' maxima and sums, then their weighted sums of V, one warp after the other
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -693,28 +700,27 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
         const float safe = top == -INFINITY ? 0.f : top;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += lw[w * R + tid] * exp2f(mw[w * R + tid] - safe);
+        for (int w = 0; w < kWarps; ++w) s += lw[w * R + tid] * ex2(mw[w * R + tid] - safe);
         mf[tid] = top;
         lf[tid] = s;
       }
       __syncthreads();
 #pragma unroll
-      for (int round = 0; round < 2; ++round) {
-        if ((warp & 1) == round) {
-          float* buf = obuf + (warp >> 1) * R * S::kObufStride;
+      for (int round = 0; round < kWarps; ++round) {
+        if (warp == round) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int r = mt * 16 + g8 + 8 * k;
               const float top = mf[r];
-              const float c = exp2f(m[mt][k] - (top == -INFINITY ? 0.f : top));
+              const float c = ex2(m[mt][k] - (top == -INFINITY ? 0.f : top));
 #pragma unroll
               for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int dim = F32 ? 32 * (j >> 2) + 4 * (2 * t4 + e) + (j & 3) : 8 * j + 2 * t4 + e;
-                  float* p = buf + r * S::kObufStride + dim;
+                  float* p = obuf + r * S::kObufStride + dim;
                   const float v = O[mt][j][2 * k + e] * c;
                   *p = round ? *p + v : v;
                 }
@@ -728,7 +734,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
         for (int i = tid; i < real * HD; i += kThreads) {
           const int r = i / HD, e = i - r * HD;
           const int rr = tile_row + r, row = rr / a.hpg, h = rr - row * a.hpg;
-          const float o = obuf[r * S::kObufStride + e] + obuf[(R + r) * S::kObufStride + e];
+          const float o = obuf[r * S::kObufStride + e];
           dst[(seq_r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * HD + e] = rounded<QT>(finish(o, lf[r], slim[r]));
         }
         if (a.scores && tid < real)
@@ -737,7 +743,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
         const long long slot = (long long)blockIdx.x * 2 + (begins_unit ? 1 : 0);
         for (int i = tid; i < real * HD; i += kThreads) {
           const int r = i / HD, e = i - r * HD;
-          a.part[(slot * R + r) * HD + e] = obuf[r * S::kObufStride + e] + obuf[(R + r) * S::kObufStride + e];
+          a.part[(slot * R + r) * HD + e] = obuf[r * S::kObufStride + e];
         }
         if (tid < real) a.ml[slot * R + tid] = make_float2(mf[tid], lf[tid]);
       }
