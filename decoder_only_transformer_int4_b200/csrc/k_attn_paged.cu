@@ -14,7 +14,7 @@
 // Split.  The positions of all (sequence, kv head, row tile) units are cut into tiles of 64 and laid
 // end to end; every resident CTA takes an equal run of tiles, whatever the lengths.  A run crosses
 // units: a unit that lies in one CTA is finished there, a cut one leaves (m, l, o) partials, one slot
-// for the piece that begins a CTA's run and one for the piece that ends it, which attn_join_kernel adds.
+// for the piece that begins a CTA's run and one for the piece that ends it, which attn_finish_kernel adds.
 // Nothing waits for another CTA, no counter has to be cleared, and the order of every sum is fixed.
 //
 // Inside a CTA each warp takes its own 16 positions of every tile and streams them with cp.async
@@ -30,6 +30,7 @@
 // sum in fp32, in the exponent's base 2.  Where the result is stored in fp32, each step's P V is summed
 // from zero and added to the running sum by a rounded addition: the tensor cores cut their sums off, which
 // over 3000 positions added up to three times the plain fp32 form's error.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -45,6 +46,8 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStep = 16;                  // positions a warp takes at a time
 constexpr int kTile = kStep * kWarps;      // positions of a tile
+constexpr int kMaxCluster = 8;            // CTAs that share a unit
+constexpr int kClusterTiles = 8;          // the most tiles each of them takes
 constexpr int kRing = 64;                  // tile descriptors a warp holds (two halves of 32)
 
 struct __align__(16) Desc {
@@ -71,6 +74,7 @@ struct Kargs {
   float* scores;                    // [batch][Hk][hpg * max_rows][capacity], or null
   float2* stats;                    // [batch][Hk][hpg * max_rows] final (max, sum), with scores
   int grid;                         // CTAs of the main kernel
+  int cluster;                      // CTAs that share a unit, 0: runs of tiles
 };
 
 // The exponent of every probability is raised by this where P enters as fp16 pairs, so that one of
@@ -233,8 +237,27 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
   pdl_wait();
   pdl_trigger();
 
-  // first tile of every sequence
-  {
+  int f0, f1, unit_b = 0, unit_kvh = 0, unit_row0 = 0;
+  if (a.cluster) {
+    // a cluster for each (sequence, kv head, row tile), an equal run of its tiles for each CTA
+    const int unit = blockIdx.x / a.cluster, rank = blockIdx.x - unit * a.cluster;
+    const int group = unit / a.rb;
+    unit_row0 = (unit - group * a.rb) * R;
+    unit_b = group / a.c.Hk;
+    unit_kvh = group - unit_b * a.c.Hk;
+    int r0, n, T;
+    seq_info(a, unit_b, r0, n, T, rank == 0 && unit_kvh == 0 && unit_row0 == 0);
+    const int per = unit_row0 < n * a.hpg ? unit_tiles(T) : 0, chunk = (per + a.cluster - 1) / a.cluster;
+    f0 = min(per, rank * chunk);
+    f1 = min(per, f0 + chunk);
+    if (tid < R) {   // what a CTA without tiles adds
+      mf[tid] = -INFINITY;
+      lf[tid] = 0.f;
+    }
+    if (f0 == f1)
+      for (int i = tid; i < R * S::kObufStride; i += kThreads) obuf[i] = 0.f;
+  } else {
+    // first tile of every sequence
     int carry = 0;
     for (int i0 = 0; i0 < B; i0 += kThreads) {
       const int i = i0 + tid;
@@ -263,14 +286,15 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     }
     if (tid == 0) pre[0] = 0;
     __syncthreads();
+    if (blockIdx.x == 0)
+      for (int i = tid; i <= B; i += kThreads) a.pre[i] = pre[i];
+    const int total = pre[B];
+    const int chunk = (total + a.grid - 1) / a.grid;
+    f0 = min((long long)total, (long long)blockIdx.x * chunk);
+    f1 = min(total, f0 + chunk);
+    if (f0 == f1) return;
   }
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= B; i += kThreads) a.pre[i] = pre[i];
-  const int total = pre[B];
-  const int chunk = (total + a.grid - 1) / a.grid;
-  const int f0 = min((long long)total, (long long)blockIdx.x * chunk), f1 = min(total, f0 + chunk);
   const int niter = f1 - f0;
-  if (niter <= 0) return;
 
   Desc* const my = descs + warp * kRing;
   unsigned char* const mystages = stages + warp * kStages * S::kStageBytes;
@@ -279,19 +303,28 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
   auto look_up = [&](int it0) {
     const int it = it0 + lane, f = f0 + it;
     if (it < niter) {
-      int lo = 0, hi = B;                  // the last sequence that begins at or before f
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= f) lo = mid;
-        else hi = mid;
+      Desc d;
+      int lo = unit_b, tile = f;
+      if (!a.cluster) {
+        lo = 0;
+        int hi = B;                        // the last sequence that begins at or before f
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (pre[mid] <= f) lo = mid;
+          else hi = mid;
+        }
       }
       const int T = a.c.lens[lo], per = unit_tiles(T);
-      const int rt = row_tiles(a, a.row_start[lo + 1] - a.row_start[lo], R);
-      const int rem = f - pre[lo], u = rem / per, tile = rem - u * per;
-      Desc d;
       d.b = lo;
-      d.kvh = u / rt;
-      d.row0 = (u - d.kvh * rt) * R;
+      d.kvh = unit_kvh;
+      d.row0 = unit_row0;
+      if (!a.cluster) {
+        const int rt = row_tiles(a, a.row_start[lo + 1] - a.row_start[lo], R);
+        const int rem = f - pre[lo], u = rem / per;
+        tile = rem - u * per;
+        d.kvh = u / rt;
+        d.row0 = (u - d.kvh * rt) * R;
+      }
       d.pos0 = tile * kTile + warp * kStep;
       d.ends = (tile == 0 ? 3 : it == 0 ? 1 : 0) | (tile == per - 1 ? 12 : it == niter - 1 ? 4 : 0);
       d.nvalid = max(0, min(kStep, T - d.pos0));
@@ -375,13 +408,20 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
       __syncthreads();   // the previous unit's rows and sums are no longer read
       seq_info(a, d.b, seq_r0, seq_n, seq_T, false);
       least = seq_T - seq_n + 1;   // positions that every row of the sequence sees
-      for (int r = warp; r < R; r += kWarps) {
-        const int rr = tile_row + r, i = rr / a.hpg, h = rr - i * a.hpg;
-        const bool real = i < seq_n;
-        const QT* src = static_cast<const QT*>(a.q) + (seq_r0 + (real ? i : 0)) * a.ldq + (long long)(kvh * a.hpg + h) * HD;
-        float x[HD / 32];
+      constexpr int kQRows = R / kWarps;
+      float xq[kQRows][HD / 32];
 #pragma unroll
-        for (int k = 0; k < HD / 32; ++k) x[k] = real ? as_float<QT>(src[k * 32 + lane]) : 0.f;
+      for (int j = 0; j < kQRows; ++j) {   // all loads first
+        const int rr = tile_row + warp + j * kWarps, i = rr / a.hpg, h = rr - i * a.hpg;
+        const QT* src = static_cast<const QT*>(a.q) + (seq_r0 + (i < seq_n ? i : 0)) * a.ldq + (long long)(kvh * a.hpg + h) * HD;
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k) xq[j][k] = i < seq_n ? as_float<QT>(src[k * 32 + lane]) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kQRows; ++j) {
+        const int r = warp + j * kWarps, i = (tile_row + r) / a.hpg;
+        const bool real = i < seq_n;
+        const float (&x)[HD / 32] = xq[j];
         float f = a.scale2;
         if constexpr (F32) {
 #pragma unroll
@@ -729,7 +769,9 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
         __syncthreads();
       }
       const int real = min(R, seq_n * a.hpg - tile_row);
-      if (begins_unit && (d.ends & 8)) {
+      if (a.cluster) {
+        // joined below
+      } else if (begins_unit && (d.ends & 8)) {
         QT* dst = static_cast<QT*>(a.out);
         for (int i = tid; i < real * HD; i += kThreads) {
           const int r = i / HD, e = i - r * HD;
@@ -749,69 +791,158 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
       }
     }
   }
+
+  if (a.cluster) {
+    // The cluster's pieces, over distributed shared memory: o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c,
+    // in the order of the CTAs; each CTA adds and stores its share of the rows.
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    int r0, n, T;
+    seq_info(a, unit_b, r0, n, T, false);
+    const int real = min(R, n * a.hpg - unit_row0), rank = cluster.block_rank();
+    QT* dst = static_cast<QT*>(a.out);
+    for (int i = rank * kThreads + tid; i < real * HD; i += a.cluster * kThreads) {
+      const int r = i / HD, e = i - r * HD;
+      const int rr = unit_row0 + r, row = rr / a.hpg, h = rr - row * a.hpg;
+      float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster], top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        const bool is = c < a.cluster;
+        m[c] = is ? *cluster.map_shared_rank(mf + r, c) : -INFINITY;
+        l[c] = is ? *cluster.map_shared_rank(lf + r, c) : 0.f;
+        o[c] = is ? *cluster.map_shared_rank(obuf + r * S::kObufStride + e, c) : 0.f;
+        top = fmaxf(top, m[c]);
+      }
+      const float safe = top == -INFINITY ? 0.f : top;
+      float so = 0.f, sl = 0.f;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        const float f = ex2(m[c] - safe);
+        sl = fmaf(f, l[c], sl);
+        so = fmaf(f, o[c], so);
+      }
+      dst[(r0 + row) * a.ldo + (long long)(unit_kvh * a.hpg + h) * HD + e] = rounded<QT>(finish(so, sl, T - n + row + 1));
+      if (a.scores && e == 0) a.stats[((long long)unit_b * a.c.Hk + unit_kvh) * (a.hpg * a.max_rows) + rr] = make_float2(top, sl);
+    }
+    cluster.sync();   // no CTA leaves while another reads its sums
+  }
 }
 
 // ---------------------------------------------------------------------------------
-// The pieces of each cut unit, added in the order of the CTAs: o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c
-// - M) l_c.  Also writes the rows of sequences that hold nothing.
+// What is left after the main kernel.  The first Hk * rb CTAs of a sequence (none after clusters) add the pieces of
+// a cut unit in the order of the CTAs, o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c, and write the rows of
+// sequences that hold nothing.  The others, if there are weights, add to w[b][g][t] the sum over the newest rows i
+// and the group's heads of 2^(s - M + bias) / L, from the scores that the main kernel left; one thread owns a
+// position, so the order of its sum is fixed.  A cut unit's M and L are worked out again by each of them: a
+// kernel between for that alone costs more than the few loads.
 // ---------------------------------------------------------------------------------
-constexpr int kJoinThreads = 256;
+constexpr int kFinishThreads = 512, kStatRows = 64;
+
+// Where the pieces of a cut unit lie: piece k is the second slot of CTA c0 (it begins the unit), or the first
+// slot of CTA c0 + k.
+struct Cut {
+  int c0, pieces;
+  __device__ __forceinline__ long long slot(int k) const { return (long long)(c0 + k) * 2 + (k == 0 ? 1 : 0); }
+};
+__device__ __forceinline__ Cut find_cut(const Kargs& a, int first, int total, int kvh, int rt, int row_tiles, int per) {
+  const int chunk = (total + a.grid - 1) / a.grid, u0 = first + (kvh * row_tiles + rt) * per;
+  Cut c;
+  c.c0 = u0 / chunk;
+  c.pieces = (u0 + per - 1) / chunk - c.c0 + 1;
+  return c;
+}
+// M and L of a row of a cut unit, by one warp
+__device__ __forceinline__ float2 cut_row(const Kargs& a, const Cut& c, int R, int r, int lane) {
+  float top = -INFINITY;
+  for (int k = lane; k < c.pieces; k += 32) top = fmaxf(top, a.ml[c.slot(k) * R + r].x);
+  top = warp_max(top);
+  const float safe = top == -INFINITY ? 0.f : top;
+  float s = 0.f;
+  for (int k = lane; k < c.pieces; k += 32) {
+    const float2 v = a.ml[c.slot(k) * R + r];
+    s = fmaf(v.y, ex2(v.x - safe), s);
+  }
+  return make_float2(top, warp_sum(s));
+}
 
 template <typename QT>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(Kargs a, int R) {
-  __shared__ float sM[32], sL[32];
-  __shared__ float4 red[kJoinThreads];
+__global__ void __launch_bounds__(kFinishThreads) attn_finish_kernel(Kargs a, int R, float* weights, long long ldw, float bias) {
+  __shared__ float sM[kStatRows], sL[kStatRows];
+  __shared__ float4 red[kFinishThreads];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kvh = blockIdx.x / a.rb, rt = blockIdx.x - kvh * a.rb, b = blockIdx.y, hd = a.c.hd;
+  const int b = blockIdx.y, hd = a.c.hd, joins = a.cluster ? 0 : a.c.Hk * a.rb;
   int r0, n, T;
   seq_info(a, b, r0, n, T, false);
-  const int row0 = rt * R, real = min(R, n * a.hpg - row0);
+  const int first = a.cluster ? 0 : a.pre[b], total = a.cluster ? 0 : a.pre[a.c.batch];
+  const int per = unit_tiles(T), rts = row_tiles(a, n, R), rows = n * a.hpg;
+  if ((int)blockIdx.x >= joins) {
+    const int chunks = (a.c.capacity() + kFinishThreads - 1) / kFinishThreads, x = blockIdx.x - joins;
+    const int g = x / chunks, t0 = (x - g * chunks) * kFinishThreads, t = t0 + tid;
+    if (t0 >= T || n <= 0) return;
+    const long long unit = (long long)b * a.c.Hk + g, most = a.hpg * a.max_rows;
+    const float* s = a.scores + unit * most * a.c.capacity() + t;
+    const int sees = max(0, t - (T - n)) * a.hpg;   // the first row that sees position t
+    float w = 0.f;
+    for (int q0 = 0; q0 < rows; q0 += kStatRows) {
+      const int q1 = min(rows, q0 + kStatRows);
+      if (q0) __syncthreads();
+      for (int q = q0 + warp; q < q1; q += kFinishThreads / 32) {
+        const int rt = q / R;
+        float2 ml;
+        Cut c{0, 1};
+        if (!a.cluster) c = find_cut(a, first, total, g, rt, rts, per);
+        if (c.pieces == 1) ml = a.stats[unit * most + q];
+        else ml = cut_row(a, c, R, q - rt * R, lane);
+        if (lane == 0) {
+          sM[q - q0] = ml.x - bias;
+          sL[q - q0] = 1.f / ml.y;
+        }
+      }
+      __syncthreads();
+      if (t < T) {
+#pragma unroll 8
+        for (int q = max(q0, sees); q < q1; ++q) w = fmaf(ex2(s[(long long)q * a.c.capacity()] - sM[q - q0]), sL[q - q0], w);
+      }
+    }
+    if (t < T) weights[unit * ldw + t] += w;
+    return;
+  }
+  const int kvh = blockIdx.x / a.rb, rt = blockIdx.x - kvh * a.rb;
+  const int row0 = rt * R, real = min(R, rows - row0);
   if (real <= 0) return;
   QT* dst = static_cast<QT*>(a.out);
   if (T == 0) {
-    for (int i = tid; i < real * hd; i += kJoinThreads) {
+    for (int i = tid; i < real * hd; i += kFinishThreads) {
       const int rr = row0 + i / hd, row = rr / a.hpg, h = rr - row * a.hpg;
       dst[(r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * hd + i % hd] = rounded<QT>(0.f);
     }
     return;
   }
-  const int per = unit_tiles(T), total = a.pre[a.c.batch], chunk = (total + a.grid - 1) / a.grid;
-  const int u0 = a.pre[b] + (kvh * row_tiles(a, n, R) + rt) * per;
-  const int c0 = u0 / chunk, c1 = (u0 + per - 1) / chunk, pieces = c1 - c0 + 1;
+  const Cut cut = find_cut(a, first, total, kvh, rt, rts, per);
+  const int pieces = cut.pieces;
   if (pieces == 1) return;
-  // piece k is the second slot of CTA c0 (it begins the unit), or the first slot of CTA c0 + k
-  auto slot = [&](int k) { return (long long)(c0 + k) * 2 + (k == 0 ? 1 : 0); };
-  for (int r = warp; r < real; r += kJoinThreads / 32) {
-    float top = -INFINITY;
-    for (int k = lane; k < pieces; k += 32) top = fmaxf(top, a.ml[slot(k) * R + r].x);
-    top = warp_max(top);
-    const float safe = top == -INFINITY ? 0.f : top;
-    float s = 0.f;
-    for (int k = lane; k < pieces; k += 32) {
-      const float2 v = a.ml[slot(k) * R + r];
-      s = fmaf(v.y, exp2f(v.x - safe), s);
-    }
-    s = warp_sum(s);
+  for (int r = warp; r < real; r += kFinishThreads / 32) {
+    const float2 ml = cut_row(a, cut, R, r, lane);
     if (lane == 0) {
-      sM[r] = safe;
-      sL[r] = s;
-      if (a.scores) a.stats[((long long)b * a.c.Hk + kvh) * (a.hpg * a.max_rows) + row0 + r] = make_float2(top, s);
+      sM[r] = ml.x == -INFINITY ? 0.f : ml.x;
+      sL[r] = ml.y;
     }
   }
   __syncthreads();
-  const int items = real * hd / 4;                               // four elements of a row each
-  const int parts = max(1, min(pieces, kJoinThreads / items));   // threads that share an item's pieces
-  for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
+  const int items = real * hd / 4;                                 // four elements of a row each
+  const int parts = max(1, min(pieces, kFinishThreads / items));   // threads that share an item's pieces
+  for (int i0 = 0; i0 < items; i0 += kFinishThreads) {
     const int part = parts > 1 ? tid / items : 0, item = parts > 1 ? tid - part * items : i0 + tid;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (item < items && part < parts) {
       const int r = item / (hd / 4), e = 4 * (item - r * (hd / 4));
-#pragma unroll 4
+#pragma unroll 8
       for (int k = part; k < pieces; k += parts) {
-        const float c = exp2f(a.ml[slot(k) * R + r].x - sM[r]);
-        const float4 x = *reinterpret_cast<const float4*>(a.part + (slot(k) * R + r) * hd + e);
+        const float c = ex2(a.ml[cut.slot(k) * R + r].x - sM[r]);
+        const float4 x = *reinterpret_cast<const float4*>(a.part + (cut.slot(k) * R + r) * hd + e);
         o.x = fmaf(c, x.x, o.x);
         o.y = fmaf(c, x.y, o.y);
         o.z = fmaf(c, x.z, o.z);
@@ -842,37 +973,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(Kargs a, int R)
   }
 }
 
-// ---------------------------------------------------------------------------------
-// w[b][g][t] += sum over the newest rows i and the group's heads of 2^(s - M + bias) / L, from the
-// scores that the main kernel left.  One thread owns a position, so the order of its sum is fixed.
-// ---------------------------------------------------------------------------------
-constexpr int kWeightThreads = 256;
-
-__global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(Kargs a, float* weights, long long ldw, float bias) {
-  pdl_wait();
-  pdl_trigger();
-  const int g = blockIdx.y, b = blockIdx.z, t = blockIdx.x * kWeightThreads + threadIdx.x;
-  int r0, n, T;
-  seq_info(a, b, r0, n, T, false);
-  if (t >= T || n <= 0) return;
-  const long long unit = (long long)b * a.c.Hk + g;
-  const int rows = n * a.hpg, most = a.hpg * a.max_rows;
-  const float* s = a.scores + unit * most * a.c.capacity() + t;
-  const float2* st = a.stats + unit * most;
-  float w = 0.f;
-  // the first row that sees position t
-  const int first = max(0, t - (T - n)) * a.hpg;
-#pragma unroll 4
-  for (int r = first; r < rows; ++r) {
-    const float2 ml = st[r];
-    w += exp2f(s[(long long)r * a.c.capacity()] - ml.x + bias) / ml.y;
-  }
-  weights[unit * ldw + t] += w;
-}
-
 // Sizes of one call, the same for the workspace and for the launch.
 struct Plan {
-  int mt, R, hpg, rb, grid;
+  int mt, R, hpg, rb, grid, cluster;
   size_t smem, part, ml, pre, stats, scores, bytes;
 };
 
@@ -888,7 +991,14 @@ Plan plan_for(const AttnPagedArgs& a, int n_sm) {
   const int fit = (int)((228 * 1024) / (p.smem + 1024));
   const int per_sm = fit < 1 ? 1 : fit > 3 ? 3 : fit;
   const long long tiles = (long long)a.c.batch * a.c.Hk * p.rb * ((a.c.capacity() + kTile - 1) / kTile);
-  p.grid = (int)(tiles < (long long)per_sm * n_sm ? tiles : (long long)per_sm * n_sm);
+  const long long resident = (long long)per_sm * n_sm;
+  // Few units that are not long: a cluster for each joins its pieces by itself, where all fit the GPU at once.
+  const long long units = (long long)a.c.batch * a.c.Hk * p.rb;
+  const int unit_most = (a.c.capacity() + kTile - 1) / kTile;
+  int C = 1;
+  while (C < kMaxCluster && C < unit_most) C *= 2;
+  p.cluster = units * C <= resident && unit_most <= kClusterTiles * C ? C : 0;
+  p.grid = (int)(p.cluster ? units * C : tiles < resident ? tiles : resident);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   p.part = 0;
   p.ml = p.part + up((size_t)p.grid * 2 * p.R * HD * 4);
@@ -924,18 +1034,22 @@ cudaError_t attn_go(const Launch& L, const AttnPagedArgs& a, int n_sm, void* ws)
   k.scores = a.weights ? reinterpret_cast<float*>(w + p.scores) : nullptr;
   k.stats = reinterpret_cast<float2*>(w + p.stats);
   k.grid = p.grid;
+  k.cluster = p.cluster;
   cudaError_t e;
+  auto main_kernel = [&](void (*kernel)(Kargs)) {
+    if (p.cluster) return launch_cluster(L, kernel, p.cluster, dim3(p.grid), dim3(kThreads), p.smem, k);
+    return launch_k(L, kernel, dim3(p.grid), dim3(kThreads), p.smem, k);
+  };
   if constexpr (sizeof(KT) == 4) {
-    e = launch_k(L, attn_paged_kernel<KT, Q32, HD, 1>, dim3(p.grid), dim3(kThreads), p.smem, k);
+    e = main_kernel(attn_paged_kernel<KT, Q32, HD, 1>);
   } else {
-    e = p.mt == 1 ? launch_k(L, attn_paged_kernel<KT, Q32, HD, 1>, dim3(p.grid), dim3(kThreads), p.smem, k)
-                  : launch_k(L, attn_paged_kernel<KT, Q32, HD, 2>, dim3(p.grid), dim3(kThreads), p.smem, k);
+    e = main_kernel(p.mt == 1 ? attn_paged_kernel<KT, Q32, HD, 1> : attn_paged_kernel<KT, Q32, HD, 2>);
   }
-  if (e != cudaSuccess) return e;
-  e = launch_k(L, attn_join_kernel<QT>, dim3(a.c.Hk * p.rb, a.c.batch), dim3(kJoinThreads), 0, k, p.R);
-  if (e != cudaSuccess || !a.weights) return e;
-  return launch_k(L, attn_weights_kernel, dim3((a.c.capacity() + kWeightThreads - 1) / kWeightThreads, a.c.Hk, a.c.batch),
-                  dim3(kWeightThreads), 0, k, a.weights, a.ldw, bias_of<KT>());
+  const int joins = p.cluster ? 0 : a.c.Hk * p.rb;
+  const int adds = a.weights ? a.c.Hk * ((a.c.capacity() + kFinishThreads - 1) / kFinishThreads) : 0;
+  if (e != cudaSuccess || joins + adds == 0) return e;
+  return launch_k(L, attn_finish_kernel<QT>, dim3(joins + adds, a.c.batch), dim3(kFinishThreads), 0, k, p.R, a.weights, a.ldw,
+                  bias_of<KT>());
 }
 
 // Calls f with the kernel family's template arguments.
