@@ -48,16 +48,15 @@ constexpr int kStep = 16;                  // positions a warp takes at a time
 constexpr int kTile = kStep * kWarps;      // positions of a tile
 constexpr int kMaxCluster = 8;            // CTAs that share a unit
 constexpr int kClusterTiles = 8;          // the most tiles each of them takes
-constexpr int kRing = 64;                  // tile descriptors a warp holds (two halves of 32)
+constexpr int kRing = 32;                  // tile descriptors a warp holds (two halves of 16)
 
-struct __align__(16) Desc {
+struct Desc {
   long long off;         // element offset of the 16 positions' first row in the pages, -1: no page there
   int pos0;              // first position
+  int row0;              // first row of the row tile
+  short b, kvh;          // sequence, kv head
   short nvalid;          // positions of the 16 that exist
   short ends;            // bits 0, 1: this tile begins the CTA's piece, the unit; bits 2, 3: ends the piece, the unit
-  int b, kvh;            // sequence, kv head
-  int row0;              // first row of the row tile
-  int unused;
 };
 
 struct Kargs {
@@ -78,19 +77,22 @@ struct Kargs {
 };
 
 // The exponent of every probability is raised by this where P enters as fp16 pairs, so that one of
-// 2^-24 keeps its lo half; it cancels in o / l.
+// 2^-20 keeps its lo half; it cancels in o / l.
 template <typename KT>
-constexpr float bias_of() { return std::is_same<KT, __half>::value ? 14.f : 0.f; }
+constexpr float bias_of() { return std::is_same<KT, __half>::value ? 10.f : 0.f; }
+// How far a score may pass the running reference before sums are scaled anew: probabilities stay below 2^14
+constexpr float kSlack = 4.f;
 
-template <typename KT, bool Q32, int HD, int MT>
+template <typename KT, bool Q32, int HD, int NB>
 struct Shape {
   static constexpr bool kF32 = sizeof(KT) == 4;
-  static constexpr int R = 16 * MT;
+  static constexpr int R = 8 * NB;
   static constexpr int kRowBytes = HD * sizeof(KT);
   static constexpr int kStageBytes = 2 * kStep * kRowBytes;      // K then V of one warp's step
   static constexpr int kStages = kStageBytes <= 4096 ? 3 : 2;
   static constexpr int kQBytes = R * HD * ((kF32 || Q32) ? 4 : 2);   // Q32 on halves: hi and lo planes
-  static constexpr int kObufStride = HD + 8;
+  static constexpr bool kQRegs = !kF32 && NB * (HD / 16) * (Q32 ? 2 : 1) <= 16;   // Q's fragments stay in registers
+  static constexpr int kObufStride = HD + 4;
   static constexpr int kObufBytes = R * kObufStride * 4;
   static constexpr int kDescBytes = kWarps * kRing * (int)sizeof(Desc);
   static constexpr int kSmall = R * 4 * (2 + 2 * kWarps + 2);
@@ -118,6 +120,12 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// the 8 x 8 matrix of 16-bit elements that a warp holds, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -209,11 +217,11 @@ __device__ __forceinline__ int row_tiles(const Kargs& a, int n, int R) { return 
 // o / l; a row that sees nothing gives 0, one whose every score is -inf gives NaN (0 / 0), as the formula
 __device__ __forceinline__ float finish(float o, float l, int lim) { return lim <= 0 ? 0.f : o / l; }
 
-template <typename KT, bool Q32, int HD, int MT>
+template <typename KT, bool Q32, int HD, int NB>
 __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
-  using S = Shape<KT, Q32, HD, MT>;
+  using S = Shape<KT, Q32, HD, NB>;
   constexpr bool F32 = S::kF32;
-  constexpr int R = S::R, NT = HD / 8, kStages = S::kStages;
+  constexpr int R = S::R, MD = HD / 16, kStages = S::kStages;
   constexpr int kCpr = S::kRowBytes / 16;          // 16-byte chunks of a row
   constexpr float kBias = bias_of<KT>();
   using QT = typename std::conditional<Q32, float, KT>::type;
@@ -299,10 +307,10 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
   Desc* const my = descs + warp * kRing;
   unsigned char* const mystages = stages + warp * kStages * S::kStageBytes;
 
-  // descriptors of tiles it0 .. it0 + 31, one per lane
+  // descriptors of tiles it0 .. it0 + 15, one per lane
   auto look_up = [&](int it0) {
     const int it = it0 + lane, f = f0 + it;
-    if (it < niter) {
+    if (lane < kRing / 2 && it < niter) {
       Desc d;
       int lo = unit_b, tile = f;
       if (!a.cluster) {
@@ -377,6 +385,12 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     cp_commit();
   };
 
+  // B fragments of row tile nb's elements 16 ks .. 16 ks + 31, from the hi (0) or the lo plane
+  auto load_q = [&](uint32_t (&t)[4], int nb, int ks, int plane) {
+    const int r = nb * 8 + (lane & 7), c = 2 * ks + (lane >> 3);
+    ldsm4(t, smem_u32(qs) + (plane * R * HD + r * HD + ((c ^ (r & 7)) << 3)) * 2);
+  };
+
   look_up(0);
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
@@ -384,9 +398,14 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     else cp_commit();
   }
 
-  float m[MT][2], l[MT][2], O[MT][NT][4];
-  float fac[MT][2];
-  int lim[MT][2];
+  // Score fragments: positions g8 + 8 (k >> 1) of the step, rows 8 nb + 2 t4 + (k & 1) of the tile; the rows of O's
+  // fragments are the same, its elements dim_of(md, k).  m is what the exponents refer to: at most kSlack below the
+  // maximum so far.
+  auto dim_of = [&](int md, int k) { return F32 ? 32 * (md >> 1) + 4 * g8 + 2 * (md & 1) + (k >> 1) : 16 * md + g8 + 8 * (k >> 1); };
+  float m[NB][2], l[NB][2], O[NB][MD][4];
+  float fac[NB][2];
+  int lim[NB][2];
+  uint32_t qreg[S::kQRegs ? NB : 1][S::kQRegs ? MD : 1][Q32 ? 4 : 2];
   int seq_r0 = 0, seq_n = 0, seq_T = 0, least = 0;
   bool begins_unit = false;
 
@@ -394,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     {
       const int nx = it + kStages - 1;
       if (nx < niter) {
-        if ((nx & 31) == 0) look_up(nx);
+        if ((nx & (kRing / 2 - 1)) == 0) look_up(nx);
         issue(nx);
       } else {
         cp_commit();
@@ -463,20 +482,31 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
       }
       __syncthreads();
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          m[mt][k] = -INFINITY;
-          l[mt][k] = 0.f;
-          fac[mt][k] = rowc[mt * 16 + g8 + 8 * k];
-          lim[mt][k] = slim[mt * 16 + g8 + 8 * k];
+          m[nb][k] = -INFINITY;
+          l[nb][k] = 0.f;
+          fac[nb][k] = rowc[nb * 8 + 2 * t4 + k];
+          lim[nb][k] = slim[nb * 8 + 2 * t4 + k];
         }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        for (int md = 0; md < MD; ++md)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+          for (int k = 0; k < 4; ++k) O[nb][md][k] = 0.f;
+        if constexpr (S::kQRegs) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) O[mt][j][k] = 0.f;
+          for (int ks = 0; ks < MD; ks += 2) {
+            uint32_t t[4];
+            load_q(t, nb, ks, 0);
+            qreg[nb][ks][0] = t[0], qreg[nb][ks][1] = t[1], qreg[nb][ks + 1][0] = t[2], qreg[nb][ks + 1][1] = t[3];
+            if constexpr (Q32) {
+              load_q(t, nb, ks, 1);
+              qreg[nb][ks][2] = t[0], qreg[nb][ks][3] = t[1], qreg[nb][ks + 1][2] = t[2], qreg[nb][ks + 1][3] = t[3];
+            }
+          }
+        }
+      }
     }
 
     cp_wait<kStages - 1>();
@@ -485,42 +515,45 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     if (d.nvalid > 0) {
       const unsigned char* kst = mystages + (it % kStages) * S::kStageBytes;
       const unsigned char* vst = kst + kStep * S::kRowBytes;
-      const uint32_t ku = smem_u32(kst), vu = smem_u32(vst), qu = smem_u32(qs);
+      const uint32_t ku = smem_u32(kst), vu = smem_u32(vst);
       // lo: the products with a lo half, where the result is stored in fp32.  They are summed apart, since
       // the tensor cores cut an addition's result off: fewer cuts fall on the large sum.
       constexpr bool kApart = F32 || Q32;
-      float sc[MT][2][4], lo[kApart ? MT : 1][2][4];
+      float sc[NB][4], lo[kApart ? NB : 1][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            sc[mt][j][k] = 0.f;
-            if constexpr (kApart) lo[mt][j][k] = 0.f;
-          }
+        for (int k = 0; k < 4; ++k) {
+          sc[nb][k] = 0.f;
+          if constexpr (kApart) lo[nb][k] = 0.f;
+        }
 
-      // S = Q K^T
+      // S^T = K Q^T
       if constexpr (!F32) {
 #pragma unroll
-        for (int ks = 0; ks < HD / 16; ++ks) {
-          uint32_t kb[4];
-          {
-            const int mi = lane >> 3, r = (lane & 7) + (mi >> 1) * 8, c = ks * 2 + (mi & 1);
-            ldsm4(kb, ku + r * S::kRowBytes + swz_k<false>(c, r) * 16);
+        for (int ks = 0; ks < MD; ks += 2) {
+          uint32_t ka[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int r = lane & 15, c = 2 * (ks + u) + (lane >> 4);
+            ldsm4(ka[u], ku + r * S::kRowBytes + swz_k<false>(c, r) * 16);
           }
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const int r = mt * 16 + (lane & 15), c = ks * 2 + (lane >> 4);
-            const uint32_t at = qu + (r * HD + ((c ^ (r & 7)) << 3)) * 2;
-            uint32_t qa[4];
-            ldsm4(qa, at);
-            mma16<KT>(sc[mt][0], qa, kb[0], kb[1]);
-            mma16<KT>(sc[mt][1], qa, kb[2], kb[3]);
+          for (int nb = 0; nb < NB; ++nb) {
+            uint32_t t[4];
+            if constexpr (!S::kQRegs) load_q(t, nb, ks, 0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if constexpr (S::kQRegs) mma16<KT>(sc[nb], ka[u], qreg[nb][ks + u][0], qreg[nb][ks + u][1]);
+              else mma16<KT>(sc[nb], ka[u], t[2 * u], t[2 * u + 1]);
+            }
             if constexpr (Q32) {
-              ldsm4(qa, at + R * HD * 2);
-              mma16<KT>(lo[mt][0], qa, kb[0], kb[1]);
-              mma16<KT>(lo[mt][1], qa, kb[2], kb[3]);
+              if constexpr (!S::kQRegs) load_q(t, nb, ks, 1);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                if constexpr (S::kQRegs) mma16<KT>(lo[nb], ka[u], qreg[nb][ks + u][2], qreg[nb][ks + u][3]);
+                else mma16<KT>(lo[nb], ka[u], t[2 * u], t[2 * u + 1]);
+              }
             }
           }
         }
@@ -528,90 +561,98 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
         // k index t of a step is element 16 j + 4 t (+ 2 in the second), k index t + 4 the one after it
 #pragma unroll 2
         for (int j = 0; j < HD / 16; ++j) {
-          const float4 q0 = *reinterpret_cast<const float4*>(qs + (g8 * HD + swz_k<true>(4 * j + t4, g8) * 4) * 4);
-          const float4 q1 = *reinterpret_cast<const float4*>(qs + ((g8 + 8) * HD + swz_k<true>(4 * j + t4, g8) * 4) * 4);
+          const float4 k0 = *reinterpret_cast<const float4*>(kst + g8 * S::kRowBytes + swz_k<true>(4 * j + t4, g8) * 16);
+          const float4 k1 = *reinterpret_cast<const float4*>(kst + (g8 + 8) * S::kRowBytes + swz_k<true>(4 * j + t4, g8) * 16);
           uint32_t ah[2][4], al[2][4];
-          split_tf32(q0.x, ah[0][0], al[0][0]);
-          split_tf32(q1.x, ah[0][1], al[0][1]);
-          split_tf32(q0.y, ah[0][2], al[0][2]);
-          split_tf32(q1.y, ah[0][3], al[0][3]);
-          split_tf32(q0.z, ah[1][0], al[1][0]);
-          split_tf32(q1.z, ah[1][1], al[1][1]);
-          split_tf32(q0.w, ah[1][2], al[1][2]);
-          split_tf32(q1.w, ah[1][3], al[1][3]);
+          split_tf32(k0.x, ah[0][0], al[0][0]);
+          split_tf32(k1.x, ah[0][1], al[0][1]);
+          split_tf32(k0.y, ah[0][2], al[0][2]);
+          split_tf32(k1.y, ah[0][3], al[0][3]);
+          split_tf32(k0.z, ah[1][0], al[1][0]);
+          split_tf32(k1.z, ah[1][1], al[1][1]);
+          split_tf32(k0.w, ah[1][2], al[1][2]);
+          split_tf32(k1.w, ah[1][3], al[1][3]);
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int r = nt * 8 + g8;
-            const float4 k4 = *reinterpret_cast<const float4*>(kst + r * S::kRowBytes + swz_k<true>(4 * j + t4, r) * 16);
+          for (int nb = 0; nb < NB; ++nb) {
+            const int r = nb * 8 + g8;
+            const float4 q4 = *reinterpret_cast<const float4*>(qs + (r * HD + swz_k<true>(4 * j + t4, r) * 4) * 4);
             uint32_t bh[4], bl[4];
-            split_tf32(k4.x, bh[0], bl[0]);
-            split_tf32(k4.y, bh[1], bl[1]);
-            split_tf32(k4.z, bh[2], bl[2]);
-            split_tf32(k4.w, bh[3], bl[3]);
+            split_tf32(q4.x, bh[0], bl[0]);
+            split_tf32(q4.y, bh[1], bl[1]);
+            split_tf32(q4.z, bh[2], bl[2]);
+            split_tf32(q4.w, bh[3], bl[3]);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-              mma8(lo[0][nt], al[s], bh[2 * s], bh[2 * s + 1]);
-              mma8(lo[0][nt], ah[s], bl[2 * s], bl[2 * s + 1]);
-              mma8(sc[0][nt], ah[s], bh[2 * s], bh[2 * s + 1]);
+              mma8(lo[nb], al[s], bh[2 * s], bh[2 * s + 1]);
+              mma8(lo[nb], ah[s], bl[2 * s], bl[2 * s + 1]);
+              mma8(sc[nb], ah[s], bh[2 * s], bh[2 * s + 1]);
             }
           }
         }
       }
 
-      // scores in base 2, masks, running maximum and sum
+      // scores in base 2, masks, reference and sum
       const bool masked = d.pos0 + kStep > least;   // some row does not see all 16
+      bool passes = false;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int k = 0; k < 4; ++k) {
+          float s = sc[nb][k];
+          if constexpr (kApart) s += lo[nb][k];
+          sc[nb][k] = s * fac[nb][k & 1];
+        }
+      if (masked) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float s = sc[mt][j][k];
-            if constexpr (kApart) s += lo[mt][j][k];
-            s *= fac[mt][k >> 1];
-            if (masked && d.pos0 + 8 * j + 2 * t4 + (k & 1) >= lim[mt][k >> 1]) s = -INFINITY;
-            sc[mt][j][k] = s;
-          }
-        if (a.scores) {
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (d.pos0 + g8 + 8 * (k >> 1) >= lim[nb][k & 1]) sc[nb][k] = -INFINITY;
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) passes |= sc[nb][k] > m[nb][k & 1] + kSlack;
+      if (a.scores) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (lim[nb][k] > 0) {   // a real row; positions behind the end fall into the capacity's last 16
+              float* dst = a.scores + (((long long)d.b * a.c.Hk + kvh) * (a.hpg * a.max_rows) + tile_row + nb * 8 + 2 * t4 + k) * a.c.capacity() + d.pos0 + g8;
+              dst[0] = sc[nb][k];
+              dst[8] = sc[nb][2 + k];
+            }
+      }
+      if (__any_sync(0xffffffffu, passes)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int rr = tile_row + mt * 16 + g8 + 8 * k;
-            if (lim[mt][k] > 0) {   // a real row; positions behind the end fall into the capacity's last 16
-              float* dst = a.scores + (((long long)d.b * a.c.Hk + kvh) * (a.hpg * a.max_rows) + rr) * a.c.capacity() + d.pos0 + 2 * t4;
-              *reinterpret_cast<float2*>(dst) = make_float2(sc[mt][0][2 * k], sc[mt][0][2 * k + 1]);
-              *reinterpret_cast<float2*>(dst + 8) = make_float2(sc[mt][1][2 * k], sc[mt][1][2 * k + 1]);
+            float top = fmaxf(sc[nb][k], sc[nb][2 + k]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float mn = fmaxf(m[nb][k], top);
+            const float c = ex2(m[nb][k] - (mn == -INFINITY ? 0.f : mn));
+            m[nb][k] = mn;
+            l[nb][k] *= c;
+#pragma unroll
+            for (int md = 0; md < MD; ++md) {
+              O[nb][md][k] *= c;
+              O[nb][md][2 + k] *= c;
             }
           }
-        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float top = fmaxf(fmaxf(sc[mt][0][2 * k], sc[mt][0][2 * k + 1]), fmaxf(sc[mt][1][2 * k], sc[mt][1][2 * k + 1]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float mn = fmaxf(m[mt][k], top);
-          const float safe = mn == -INFINITY ? 0.f : mn;
-          if (__any_sync(0xffffffffu, mn > m[mt][k])) {
-            const float c = ex2(m[mt][k] - safe);
-            l[mt][k] *= c;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              O[mt][j][2 * k] *= c;
-              O[mt][j][2 * k + 1] *= c;
-            }
-          }
-          m[mt][k] = mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p = ex2(sc[mt][j][2 * k + e] - safe + kBias);
-              sc[mt][j][2 * k + e] = p;
-              sum += p;
-            }
-          l[mt][k] += sum;
+          const float from = kBias - (m[nb][k] == -INFINITY ? 0.f : m[nb][k]);
+          sc[nb][k] = ex2(sc[nb][k] + from);
+          sc[nb][2 + k] = ex2(sc[nb][2 + k] + from);
+          l[nb][k] += sc[nb][k] + sc[nb][2 + k];
         }
-      }
 
       // A masked row takes nothing from a position it does not see, but 0 x inf is NaN: where such
       // positions hold a V that is not finite, the step's P V is added element by element.
@@ -625,111 +666,121 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
           }
         odd = __any_sync(0xffffffffu, odd);
       }
+      // O^T += V^T P^T
       if (odd) {
         for (int r = 0; r < d.nvalid; ++r)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int nb = 0; nb < NB; ++nb) {
             float p[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float x0 = r & 8 ? sc[mt][1][2 * k] : sc[mt][0][2 * k];
-              const float x1 = r & 8 ? sc[mt][1][2 * k + 1] : sc[mt][0][2 * k + 1];
-              p[k] = __shfl_sync(0xffffffffu, r & 1 ? x1 : x0, (lane & ~3) | ((r & 7) >> 1));
-            }
+            for (int k = 0; k < 2; ++k) p[k] = __shfl_sync(0xffffffffu, r & 8 ? sc[nb][2 + k] : sc[nb][k], ((r & 7) << 2) | t4);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int md = 0; md < MD; ++md)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const int e = F32 ? 32 * (j >> 2) + 4 * (2 * t4 + (k & 1)) + (j & 3) : 8 * j + 2 * t4 + (k & 1);
+                const int e = dim_of(md, k);
                 const int c = e * (int)sizeof(KT) / 16;
                 const float x = staged<KT>(vst + r * S::kRowBytes + swz_v<F32>(c, r) * 16 + e * sizeof(KT) % 16);
-                if (d.pos0 + r < lim[mt][k >> 1]) O[mt][j][k] = fmaf(p[k >> 1], x, O[mt][j][k]);
+                if (d.pos0 + r < lim[nb][k & 1]) O[nb][md][k] = fmaf(p[k & 1], x, O[nb][md][k]);
               }
           }
       } else if constexpr (!F32) {
-        uint32_t ph[MT][4], pl[MT][4];
+        uint32_t ph[NB][2], pl[NB][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // A fragment: registers (rows g, positions 2t), (rows g + 8, 2t), (g, 8 + 2t), (g + 8, 8 + 2t)
-            const int j = i >> 1, k = i & 1;
+          for (int i = 0; i < 2; ++i) {
             float ra, rb, za, zb;
-            ph[mt][i] = Two<KT>::pack(sc[mt][j][2 * k], sc[mt][j][2 * k + 1], ra, rb);
-            pl[mt][i] = Two<KT>::pack(ra, rb, za, zb);
+            const uint32_t h = Two<KT>::pack(sc[nb][2 * i], sc[nb][2 * i + 1], ra, rb);
+            const uint32_t w = Two<KT>::pack(ra, rb, za, zb);
+            ph[nb][i] = transpose8(h);   // positions 2 t4, 2 t4 + 1 (+ 8 i) of row g8: a B fragment
+            pl[nb][i] = transpose8(w);
           }
 #pragma unroll
-        for (int j = 0; j < NT / 2; ++j) {
-          uint32_t vb[4];
-          const int r = lane & 15, c = 2 * j + (lane >> 4);
-          ldsm4t(vb, vu + r * S::kRowBytes + swz_v<false>(c, r) * 16);
+        for (int md = 0; md < MD; ++md) {
+          uint32_t va[4];
+          const int r = (lane & 7) + 8 * (lane >> 4), c = 2 * md + ((lane >> 3) & 1);
+          ldsm4t(va, vu + r * S::kRowBytes + swz_v<false>(c, r) * 16);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int nb = 0; nb < NB; ++nb) {
             if constexpr (Q32) {
-              float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16<KT>(d0, pl[mt], vb[0], vb[1]);
-              mma16<KT>(d1, pl[mt], vb[2], vb[3]);
-              mma16<KT>(d0, ph[mt], vb[0], vb[1]);
-              mma16<KT>(d1, ph[mt], vb[2], vb[3]);
+              float x[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16<KT>(x, va, pl[nb][0], pl[nb][1]);
+              mma16<KT>(x, va, ph[nb][0], ph[nb][1]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                O[mt][2 * j][k] += d0[k];
-                O[mt][2 * j + 1][k] += d1[k];
-              }
+              for (int k = 0; k < 4; ++k) O[nb][md][k] += x[k];
             } else {
-              mma16<KT>(O[mt][2 * j], ph[mt], vb[0], vb[1]);
-              mma16<KT>(O[mt][2 * j + 1], ph[mt], vb[2], vb[3]);
-              mma16<KT>(O[mt][2 * j], pl[mt], vb[0], vb[1]);
-              mma16<KT>(O[mt][2 * j + 1], pl[mt], vb[2], vb[3]);
+              mma16<KT>(O[nb][md], va, ph[nb][0], ph[nb][1]);
+              mma16<KT>(O[nb][md], va, pl[nb][0], pl[nb][1]);
             }
           }
         }
       } else {
-        // k index t is position 8 nt + 2 t, t + 4 the one after it; column n of tile 4 J + jj is
-        // element 32 J + 4 n + jj, so that a lane's V loads are 16 bytes
+        // k index t is position 8 nt + 2 t, t + 4 the one after it
+        uint32_t bh[NB][4], bl[NB][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          uint32_t ah[4], al[4];
-          split_tf32(sc[0][nt][0], ah[0], al[0]);
-          split_tf32(sc[0][nt][2], ah[1], al[1]);
-          split_tf32(sc[0][nt][1], ah[2], al[2]);
-          split_tf32(sc[0][nt][3], ah[3], al[3]);
-          const int ra = 8 * nt + 2 * t4, rb = ra + 1;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int J = 0; J < HD / 32; ++J) {
-            const float4 x = *reinterpret_cast<const float4*>(vst + ra * S::kRowBytes + swz_v<true>(8 * J + g8, ra) * 16);
-            const float4 y = *reinterpret_cast<const float4*>(vst + rb * S::kRowBytes + swz_v<true>(8 * J + g8, rb) * 16);
-            const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+          for (int i = 0; i < 4; ++i) {
+            // lane (g8, t4) takes row g8's probability of position 8 (i >> 1) + 2 t4 + (i & 1)
+            const int from = (2 * t4 + (i & 1)) * 4 + (g8 >> 1);
+            const float even = __shfl_sync(0xffffffffu, sc[nb][i & 2], from), uneven = __shfl_sync(0xffffffffu, sc[nb][(i & 2) + 1], from);
+            split_tf32(g8 & 1 ? uneven : even, bh[nb][i], bl[nb][i]);
+          }
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-              uint32_t xh, xl, yh, yl;
-              split_tf32(xs[jj], xh, xl);
-              split_tf32(ys[jj], yh, yl);
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-              mma8(d, al, xh, yh);
-              mma8(d, ah, xl, yl);
-              mma8(d, ah, xh, yh);
+        for (int J = 0; J < HD / 32; ++J) {
+          float x[NB][2][4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) O[0][4 * J + jj][k] += d[k];
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[nb][u][k] = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const int ra = 8 * nt + 2 * t4, rb = ra + 1;
+            const float4 y = *reinterpret_cast<const float4*>(vst + ra * S::kRowBytes + swz_v<true>(8 * J + g8, ra) * 16);
+            const float4 z = *reinterpret_cast<const float4*>(vst + rb * S::kRowBytes + swz_v<true>(8 * J + g8, rb) * 16);
+            const float ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t vh[4], vl[4];
+              split_tf32(ys[2 * u], vh[0], vl[0]);
+              split_tf32(ys[2 * u + 1], vh[1], vl[1]);
+              split_tf32(zs[2 * u], vh[2], vl[2]);
+              split_tf32(zs[2 * u + 1], vh[3], vl[3]);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                mma8(x[nb][u], vl, bh[nb][2 * nt], bh[nb][2 * nt + 1]);
+                mma8(x[nb][u], vh, bl[nb][2 * nt], bl[nb][2 * nt + 1]);
+                mma8(x[nb][u], vh, bh[nb][2 * nt], bh[nb][2 * nt + 1]);
+              }
             }
           }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) O[nb][2 * J + u][k] += x[nb][u][k];
         }
       }
     }
     __syncwarp();   // the ring's next copy goes into this stage
 
     if (d.ends & 4) {
-      // the four warps' maxima and sums, then their weighted sums of V, one warp after the other
+      // the four warps' references and sums, then their weighted sums of V, one warp after the other
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float s = l[mt][k];
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);
-          if (t4 == 0) {
-            mw[warp * R + mt * 16 + g8 + 8 * k] = m[mt][k];
-            lw[warp * R + mt * 16 + g8 + 8 * k] = s;
+          float s = l[nb][k];
+          s += __shfl_xor_sync(0xffffffffu, s, 4);
+          s += __shfl_xor_sync(0xffffffffu, s, 8);
+          s += __shfl_xor_sync(0xffffffffu, s, 16);
+          if (g8 == 0) {
+            mw[warp * R + nb * 8 + 2 * t4 + k] = m[nb][k];
+            lw[warp * R + nb * 8 + 2 * t4 + k] = s;
           }
         }
       __syncthreads();
@@ -745,26 +796,27 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
         lf[tid] = s;
       }
       __syncthreads();
+      float scale[NB][2];
 #pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float top = mf[nb * 8 + 2 * t4 + k];
+          scale[nb][k] = ex2(m[nb][k] - (top == -INFINITY ? 0.f : top));
+        }
+#pragma unroll 1
       for (int round = 0; round < kWarps; ++round) {
         if (warp == round) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int r = mt * 16 + g8 + 8 * k;
-              const float top = mf[r];
-              const float c = ex2(m[mt][k] - (top == -INFINITY ? 0.f : top));
+            for (int md = 0; md < MD; ++md)
 #pragma unroll
-              for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int dim = F32 ? 32 * (j >> 2) + 4 * (2 * t4 + e) + (j & 3) : 8 * j + 2 * t4 + e;
-                  float* p = obuf + r * S::kObufStride + dim;
-                  const float v = O[mt][j][2 * k + e] * c;
-                  *p = round ? *p + v : v;
-                }
-            }
+              for (int k = 0; k < 4; ++k) {
+                float* p = obuf + (nb * 8 + 2 * t4 + (k & 1)) * S::kObufStride + dim_of(md, k);
+                const float v = O[nb][md][k] * scale[nb][k & 1];
+                *p = round ? *p + v : v;
+              }
         }
         __syncthreads();
       }
@@ -973,9 +1025,23 @@ __global__ void __launch_bounds__(kFinishThreads) attn_finish_kernel(Kargs a, in
   }
 }
 
+// Row tiles that one pass over the cache serves: 4 fill the registers at 128 elements a head (128 sums a thread), fp32 needs
+// more beside them.
+template <typename KT>
+constexpr int kMostTiles = sizeof(KT) == 4 ? 2 : 4;
+// f with the number of row tiles as a type
+template <typename KT, typename F>
+auto with_nb(int nb, F&& f) {
+  if constexpr (kMostTiles<KT> > 2) {
+    if (nb == 4) return f(std::integral_constant<int, 4>());
+    if (nb == 3) return f(std::integral_constant<int, 3>());
+  }
+  return nb == 2 ? f(std::integral_constant<int, 2>()) : f(std::integral_constant<int, 1>());
+}
+
 // Sizes of one call, the same for the workspace and for the launch.
 struct Plan {
-  int mt, R, hpg, rb, grid, cluster;
+  int nb, R, hpg, rb, grid, cluster;
   size_t smem, part, ml, pre, stats, scores, bytes;
 };
 
@@ -984,10 +1050,12 @@ Plan plan_for(const AttnPagedArgs& a, int n_sm) {
   Plan p;
   p.hpg = a.H / a.c.Hk;
   const long long rows = (long long)p.hpg * a.max_rows;
-  p.mt = sizeof(KT) == 4 || rows <= 16 ? 1 : 2;
-  p.R = 16 * p.mt;
-  p.rb = (int)((rows + p.R - 1) / p.R);
-  p.smem = p.mt == 1 ? Shape<KT, Q32, HD, 1>::smem(a.c.batch) : Shape<KT, Q32, HD, 2>::smem(a.c.batch);
+  // rows in tiles of 8, up to kMostTiles a pass over the cache, as even as they go
+  const int pass = kMostTiles<KT> * 8;
+  p.rb = (int)((rows + pass - 1) / pass);
+  p.nb = (int)((rows + p.rb * 8 - 1) / (p.rb * 8));
+  p.R = 8 * p.nb;
+  p.smem = with_nb<KT>(p.nb, [&](auto nb) { return Shape<KT, Q32, HD, decltype(nb)::value>::smem(a.c.batch); });
   const int fit = (int)((228 * 1024) / (p.smem + 1024));
   const int per_sm = fit < 1 ? 1 : fit > 3 ? 3 : fit;
   const long long tiles = (long long)a.c.batch * a.c.Hk * p.rb * ((a.c.capacity() + kTile - 1) / kTile);
@@ -1036,15 +1104,11 @@ cudaError_t attn_go(const Launch& L, const AttnPagedArgs& a, int n_sm, void* ws)
   k.grid = p.grid;
   k.cluster = p.cluster;
   cudaError_t e;
-  auto main_kernel = [&](void (*kernel)(Kargs)) {
+  e = with_nb<KT>(p.nb, [&](auto nb) {
+    const auto kernel = attn_paged_kernel<KT, Q32, HD, decltype(nb)::value>;
     if (p.cluster) return launch_cluster(L, kernel, p.cluster, dim3(p.grid), dim3(kThreads), p.smem, k);
     return launch_k(L, kernel, dim3(p.grid), dim3(kThreads), p.smem, k);
-  };
-  if constexpr (sizeof(KT) == 4) {
-    e = main_kernel(attn_paged_kernel<KT, Q32, HD, 1>);
-  } else {
-    e = main_kernel(p.mt == 1 ? attn_paged_kernel<KT, Q32, HD, 1> : attn_paged_kernel<KT, Q32, HD, 2>);
-  }
+  });
   const int joins = p.cluster ? 0 : a.c.Hk * p.rb;
   const int adds = a.weights ? a.c.Hk * ((a.c.capacity() + kFinishThreads - 1) / kFinishThreads) : 0;
   if (e != cudaSuccess || joins + adds == 0) return e;
@@ -1077,9 +1141,12 @@ struct DoLaunch {
 };
 struct DoAttrs {
   template <typename KT, bool Q32, int HD> cudaError_t operator()() {
-    cudaError_t e = allow_smem(attn_paged_kernel<KT, Q32, HD, 1>, Shape<KT, Q32, HD, 1>::smem(kPagedMaxBatch));
-    if constexpr (sizeof(KT) == 2)
-      if (e == cudaSuccess) e = allow_smem(attn_paged_kernel<KT, Q32, HD, 2>, Shape<KT, Q32, HD, 2>::smem(kPagedMaxBatch));
+    cudaError_t e = cudaSuccess;
+    for (int i = 1; i <= kMostTiles<KT> && e == cudaSuccess; ++i)
+      e = with_nb<KT>(i, [&](auto nb) {
+        constexpr int NB = decltype(nb)::value;
+        return allow_smem(attn_paged_kernel<KT, Q32, HD, NB>, Shape<KT, Q32, HD, NB>::smem(kPagedMaxBatch));
+      });
     return e;
   }
 };
