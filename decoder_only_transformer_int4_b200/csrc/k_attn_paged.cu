@@ -47,7 +47,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStep = 16;                  // positions a warp takes at a time
 constexpr int kTile = kStep * kWarps;      // positions of a tile
 constexpr int kMaxCluster = 8;            // CTAs that share a unit
-constexpr int kClusterTiles = 8;          // the most tiles each of them takes
+constexpr int kClusterTiles = 2;          // the most tiles each of them takes
 constexpr int kRing = 32;                  // tile descriptors a warp holds (two halves of 16)
 
 struct Desc {
@@ -69,11 +69,11 @@ struct Kargs {
   float scale2;                     // scale * log2(e)
   float* part;                      // [CTAs][2][R][hd] unscaled sums of cut units
   float2* ml;                       // [CTAs][2][R] their (max, sum)
-  int* pre;                         // [batch + 1] first tile of each sequence, for the later kernels
   float* scores;                    // [batch][Hk][hpg * max_rows][capacity], or null
   float2* stats;                    // [batch][Hk][hpg * max_rows] final (max, sum), with scores
   int grid;                         // CTAs of the main kernel
   int cluster;                      // CTAs that share a unit, 0: runs of tiles
+  int slices;                       // CTAs that join a unit's pieces
 };
 
 // The exponent of every probability is raised by this where P enters as fp16 pairs, so that one of
@@ -294,8 +294,6 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     }
     if (tid == 0) pre[0] = 0;
     __syncthreads();
-    if (blockIdx.x == 0)
-      for (int i = tid; i <= B; i += kThreads) a.pre[i] = pre[i];
     const int total = pre[B];
     const int chunk = (total + a.grid - 1) / a.grid;
     f0 = min((long long)total, (long long)blockIdx.x * chunk);
@@ -808,15 +806,19 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
       for (int round = 0; round < kWarps; ++round) {
         if (warp == round) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NB; ++nb) {
+            float* const rows = obuf + (nb * 8 + 2 * t4) * S::kObufStride;
+            float was[MD][4];   // all loads of a row tile before its stores
 #pragma unroll
             for (int md = 0; md < MD; ++md)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float* p = obuf + (nb * 8 + 2 * t4 + (k & 1)) * S::kObufStride + dim_of(md, k);
-                const float v = O[nb][md][k] * scale[nb][k & 1];
-                *p = round ? *p + v : v;
-              }
+              for (int k = 0; k < 4; ++k) was[md][k] = round ? rows[(k & 1) * S::kObufStride + dim_of(md, k)] : 0.f;
+#pragma unroll
+            for (int md = 0; md < MD; ++md)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                rows[(k & 1) * S::kObufStride + dim_of(md, k)] = fmaf(O[nb][md][k], scale[nb][k & 1], was[md][k]);
+          }
         }
         __syncthreads();
       }
@@ -882,17 +884,23 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
 }
 
 // ---------------------------------------------------------------------------------
-// What is left after the main kernel.  The first Hk * rb CTAs of a sequence (none after clusters) add the pieces of
-// a cut unit in the order of the CTAs, o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c, and write the rows of
-// sequences that hold nothing.  The others, if there are weights, add to w[b][g][t] the sum over the newest rows i
-// and the group's heads of 2^(s - M + bias) / L, from the scores that the main kernel left; one thread owns a
-// position, so the order of its sum is fixed.  A cut unit's M and L are worked out again by each of them: a
-// kernel between for that alone costs more than the few loads.
+// What is left after the main kernel.  The first CTAs of a sequence (none after clusters), some for
+// each unit, add the pieces of a cut unit in the order of the CTAs, o = sum_c 2^(m_c - M) o_c /
+// sum_c 2^(m_c - M) l_c, and write the rows of sequences that hold nothing.  The others, if there are weights, add to
+// w[b][g][t] the sum over the newest rows i and the group's heads of 2^(s - M + bias) / L, from the scores that the
+// main kernel left; one thread owns a position, so the order of its sum is fixed.  A cut unit's M and L are worked out
+// again by each of them: a kernel between for that alone costs more than the few loads.
+//
+// Latency is all there is to it, so it starts while the main kernel still runs: lengths and row ranges (inputs
+// of the main kernel, whose CTAs have all seen the kernels before it end) are read and the tiles counted before the
+// wait, and after it every load but those of the cut rows' (M, L) is issued at once.  A CTA that finds
+// nothing to do leaves before the wait; CTA 0 stays for it, so that this grid does not end before the main one.
 // ---------------------------------------------------------------------------------
-constexpr int kFinishThreads = 512, kStatRows = 64;
+constexpr int kFinishThreads = 256, kFinishWarps = kFinishThreads / 32, kStatRows = 64;
+constexpr int kWeightTile = 1024;   // positions of a weighing CTA
+constexpr int kLeastSlice = 16;   // elements of a head that a joining CTA writes, at least
 
-// Where the pieces of a cut unit lie: piece k is the second slot of CTA c0 (it begins the unit), or the first
-// slot of CTA c0 + k.
+// The pieces of a cut unit: piece k is the second slot of CTA c0 (it begins the unit), or the first slot of CTA c0 + k.
 struct Cut {
   int c0, pieces;
   __device__ __forceinline__ long long slot(int k) const { return (long long)(c0 + k) * 2 + (k == 0 ? 1 : 0); }
@@ -906,122 +914,208 @@ __device__ __forceinline__ Cut find_cut(const Kargs& a, int first, int total, in
 }
 // M and L of a row of a cut unit, by one warp
 __device__ __forceinline__ float2 cut_row(const Kargs& a, const Cut& c, int R, int r, int lane) {
-  float top = -INFINITY;
-  for (int k = lane; k < c.pieces; k += 32) top = fmaxf(top, a.ml[c.slot(k) * R + r].x);
-  top = warp_max(top);
-  const float safe = top == -INFINITY ? 0.f : top;
-  float s = 0.f;
-  for (int k = lane; k < c.pieces; k += 32) {
-    const float2 v = a.ml[c.slot(k) * R + r];
-    s = fmaf(v.y, ex2(v.x - safe), s);
+  constexpr int U = 4;
+  float top = -INFINITY, sum = 0.f;   // of this lane's pieces
+  for (int k0 = lane; k0 < c.pieces; k0 += 32 * U) {
+    float2 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 32 * u;
+      v[u] = k < c.pieces ? a.ml[c.slot(k) * R + r] : make_float2(-INFINITY, 0.f);
+    }
+    float most = top;
+#pragma unroll
+    for (int u = 0; u < U; ++u) most = fmaxf(most, v[u].x);
+    const float safe = most == -INFINITY ? 0.f : most;
+    sum *= ex2(top - safe);
+#pragma unroll
+    for (int u = 0; u < U; ++u) sum = fmaf(v[u].y, ex2(v[u].x - safe), sum);
+    top = most;
   }
-  return make_float2(top, warp_sum(s));
+  const float all = warp_max(top);
+  return make_float2(all, warp_sum(sum * ex2(top - (all == -INFINITY ? 0.f : all))));
 }
 
 template <typename QT>
 __global__ void __launch_bounds__(kFinishThreads) attn_finish_kernel(Kargs a, int R, float* weights, long long ldw, float bias) {
   __shared__ float sM[kStatRows], sL[kStatRows];
   __shared__ float4 red[kFinishThreads];
-  pdl_wait();
-  pdl_trigger();
+  __shared__ int counts[2][kFinishWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.y, hd = a.c.hd, joins = a.cluster ? 0 : a.c.Hk * a.rb;
+  const int b = blockIdx.y, hd = a.c.hd, slices = a.slices, joins = a.cluster ? 0 : a.c.Hk * a.rb * slices;
   int r0, n, T;
   seq_info(a, b, r0, n, T, false);
-  const int first = a.cluster ? 0 : a.pre[b], total = a.cluster ? 0 : a.pre[a.c.batch];
+  int first = 0, total = 0;   // tiles before this sequence's, tiles of all
+  if (!a.cluster) {
+    for (int i = tid; i < a.c.batch; i += kFinishThreads) {
+      int ri, ni, Ti;
+      seq_info(a, i, ri, ni, Ti, false);
+      const int mine = unit_tiles(Ti) * row_tiles(a, ni, R) * a.c.Hk;
+      total += mine;
+      if (i < b) first += mine;
+    }
+    first = __reduce_add_sync(0xffffffffu, first);
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) {
+      counts[0][warp] = first;
+      counts[1][warp] = total;
+    }
+    __syncthreads();
+    first = total = 0;
+#pragma unroll
+    for (int w = 0; w < kFinishWarps; ++w) {
+      first += counts[0][w];
+      total += counts[1][w];
+    }
+  }
   const int per = unit_tiles(T), rts = row_tiles(a, n, R), rows = n * a.hpg;
+  auto leave = [&] {
+    if (blockIdx.x == 0 && b == 0) pdl_wait();
+    pdl_trigger();
+  };
+
   if ((int)blockIdx.x >= joins) {
-    const int chunks = (a.c.capacity() + kFinishThreads - 1) / kFinishThreads, x = blockIdx.x - joins;
-    const int g = x / chunks, t0 = (x - g * chunks) * kFinishThreads, t = t0 + tid;
-    if (t0 >= T || n <= 0) return;
+    const int chunks = (a.c.capacity() + kWeightTile - 1) / kWeightTile, x = blockIdx.x - joins;
+    const int g = x / chunks, t0 = (x - g * chunks) * kWeightTile;
+    if (t0 >= T || n <= 0) return leave();
     const long long unit = (long long)b * a.c.Hk + g, most = a.hpg * a.max_rows;
-    const float* s = a.scores + unit * most * a.c.capacity() + t;
-    const int sees = max(0, t - (T - n)) * a.hpg;   // the first row that sees position t
-    float w = 0.f;
+    const float* s = a.scores + unit * most * a.c.capacity();
+    float* to = weights + unit * ldw;
+    constexpr int P = kWeightTile / kFinishThreads, U = 4;   // positions a thread, rows at a time
+    int t[P], sees[P];                                       // the first row that sees position t
+    float was[P], w[P], v[U][P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      t[p] = t0 + p * kFinishThreads + tid;
+      sees[p] = t[p] < T ? max(0, t[p] - (T - n)) * a.hpg : rows;
+      w[p] = 0.f;
+    }
+    pdl_wait();
+    pdl_trigger();
+    auto load = [&](int q, int q1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          v[u][p] = q + u >= sees[p] && q + u < q1 ? s[(long long)(q + u) * a.c.capacity() + t[p]] : 0.f;
+    };
+#pragma unroll
+    for (int p = 0; p < P; ++p) was[p] = t[p] < T ? to[t[p]] : 0.f;
     for (int q0 = 0; q0 < rows; q0 += kStatRows) {
       const int q1 = min(rows, q0 + kStatRows);
+      load(q0, q1);
       if (q0) __syncthreads();
-      for (int q = q0 + warp; q < q1; q += kFinishThreads / 32) {
+      for (int q = q0 + warp; q < q1; q += kFinishWarps) {
         const int rt = q / R;
-        float2 ml;
         Cut c{0, 1};
         if (!a.cluster) c = find_cut(a, first, total, g, rt, rts, per);
-        if (c.pieces == 1) ml = a.stats[unit * most + q];
-        else ml = cut_row(a, c, R, q - rt * R, lane);
+        const float2 ml = c.pieces == 1 ? a.stats[unit * most + q] : cut_row(a, c, R, q - rt * R, lane);
         if (lane == 0) {
           sM[q - q0] = ml.x - bias;
           sL[q - q0] = 1.f / ml.y;
         }
       }
       __syncthreads();
-      if (t < T) {
-#pragma unroll 8
-        for (int q = max(q0, sees); q < q1; ++q) w = fmaf(ex2(s[(long long)q * a.c.capacity()] - sM[q - q0]), sL[q - q0], w);
+      for (int q = q0; q < q1; q += U) {
+        if (q != q0) load(q, q1);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            if (q + u >= sees[p] && q + u < q1) w[p] = fmaf(ex2(v[u][p] - sM[q + u - q0]), sL[q + u - q0], w[p]);
       }
     }
-    if (t < T) weights[unit * ldw + t] += w;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if (t[p] < T) to[t[p]] = was[p] + w[p];
     return;
   }
-  const int kvh = blockIdx.x / a.rb, rt = blockIdx.x - kvh * a.rb;
+  const int unit = blockIdx.x / slices, slice = hd / slices, e0 = (blockIdx.x - unit * slices) * slice;
+  const int kvh = unit / a.rb, rt = unit - kvh * a.rb;
   const int row0 = rt * R, real = min(R, rows - row0);
-  if (real <= 0) return;
-  QT* dst = static_cast<QT*>(a.out);
+  if (real <= 0) return leave();
+  const int vecs = slice / 4, items = real * vecs;   // four elements of a row each
+  auto out = [&](int r, int e) {
+    const int rr = row0 + r, row = rr / a.hpg, h = rr - row * a.hpg;
+    return static_cast<QT*>(a.out) + (r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * hd + e;
+  };
   if (T == 0) {
-    for (int i = tid; i < real * hd; i += kFinishThreads) {
-      const int rr = row0 + i / hd, row = rr / a.hpg, h = rr - row * a.hpg;
-      dst[(r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * hd + i % hd] = rounded<QT>(0.f);
-    }
+    pdl_wait();   // rows may be read before the main kernel by none of ours, but order their writes all the same
+    pdl_trigger();
+    for (int i = tid; i < items; i += kFinishThreads)
+      for (int k = 0; k < 4; ++k) out(i / vecs, e0 + 4 * (i % vecs))[k] = rounded<QT>(0.f);
     return;
   }
   const Cut cut = find_cut(a, first, total, kvh, rt, rts, per);
   const int pieces = cut.pieces;
-  if (pieces == 1) return;
-  for (int r = warp; r < real; r += kFinishThreads / 32) {
-    const float2 ml = cut_row(a, cut, R, r, lane);
+  if (pieces == 1) return leave();
+  // threads that share an item's pieces, or items a thread
+  const int parts = max(1, min(pieces, kFinishThreads / items)), part = parts > 1 ? tid / items : 0;
+  int item = parts > 1 ? tid - part * items : tid, r = item / vecs, e = e0 + 4 * (item - r * vecs);
+  constexpr int U = 4;
+  pdl_wait();
+  pdl_trigger();
+  float4 x[U];
+  float m[U];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * parts;
+      const bool is = part < parts && item < items && k < pieces;
+      x[u] = is ? *reinterpret_cast<const float4*>(a.part + (cut.slot(k) * R + r) * hd + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      m[u] = is ? a.ml[cut.slot(k) * R + r].x : -INFINITY;
+    }
+  };
+  load(part);
+  for (int q = warp; q < real; q += kFinishWarps) {
+    const float2 ml = cut_row(a, cut, R, q, lane);
     if (lane == 0) {
-      sM[r] = ml.x == -INFINITY ? 0.f : ml.x;
-      sL[r] = ml.y;
+      sM[q] = ml.x == -INFINITY ? 0.f : ml.x;
+      sL[q] = ml.y;
     }
   }
   __syncthreads();
-  const int items = real * hd / 4;                                 // four elements of a row each
-  const int parts = max(1, min(pieces, kFinishThreads / items));   // threads that share an item's pieces
-  for (int i0 = 0; i0 < items; i0 += kFinishThreads) {
-    const int part = parts > 1 ? tid / items : 0, item = parts > 1 ? tid - part * items : i0 + tid;
+  while (true) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (item < items && part < parts) {
-      const int r = item / (hd / 4), e = 4 * (item - r * (hd / 4));
-#pragma unroll 8
-      for (int k = part; k < pieces; k += parts) {
-        const float c = ex2(a.ml[cut.slot(k) * R + r].x - sM[r]);
-        const float4 x = *reinterpret_cast<const float4*>(a.part + (cut.slot(k) * R + r) * hd + e);
-        o.x = fmaf(c, x.x, o.x);
-        o.y = fmaf(c, x.y, o.y);
-        o.z = fmaf(c, x.z, o.z);
-        o.w = fmaf(c, x.w, o.w);
+    if (part < parts && item < items) {
+      const float M = sM[r];
+      for (int k = part; k < pieces; k += U * parts) {
+        if (k != part) load(k);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float c = ex2(m[u] - M);
+          o.x = fmaf(c, x[u].x, o.x);
+          o.y = fmaf(c, x[u].y, o.y);
+          o.z = fmaf(c, x[u].z, o.z);
+          o.w = fmaf(c, x[u].w, o.w);
+        }
       }
     }
     if (parts > 1) {
       red[tid] = o;
       __syncthreads();
-      if (tid < items)
+      if (part == 0)
         for (int p = 1; p < parts; ++p) {
-          const float4 x = red[tid + p * items];
-          o.x += x.x;
-          o.y += x.y;
-          o.z += x.z;
-          o.w += x.w;
+          const float4 y = red[tid + p * items];
+          o.x += y.x;
+          o.y += y.y;
+          o.z += y.z;
+          o.w += y.w;
         }
     }
-    if (item < items && part == 0) {
-      const int r = item / (hd / 4), e = 4 * (item - r * (hd / 4));
-      const int rr = row0 + r, row = rr / a.hpg, h = rr - row * a.hpg, lim = T - n + row + 1;
-      QT* p = dst + (r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * hd + e;
-      p[0] = rounded<QT>(finish(o.x, sL[r], lim));
-      p[1] = rounded<QT>(finish(o.y, sL[r], lim));
-      p[2] = rounded<QT>(finish(o.z, sL[r], lim));
-      p[3] = rounded<QT>(finish(o.w, sL[r], lim));
+    if (part == 0 && item < items) {
+      const int lim = T - n + (row0 + r) / a.hpg + 1;
+      QT* to = out(r, e);
+      to[0] = rounded<QT>(finish(o.x, sL[r], lim));
+      to[1] = rounded<QT>(finish(o.y, sL[r], lim));
+      to[2] = rounded<QT>(finish(o.z, sL[r], lim));
+      to[3] = rounded<QT>(finish(o.w, sL[r], lim));
     }
+    item += kFinishThreads;
+    if (parts > 1 || item >= items) return;
+    r = item / vecs;
+    e = e0 + 4 * (item - r * vecs);
+    load(0);
   }
 }
 
@@ -1042,7 +1136,7 @@ auto with_nb(int nb, F&& f) {
 // Sizes of one call, the same for the workspace and for the launch.
 struct Plan {
   int nb, R, hpg, rb, grid, cluster;
-  size_t smem, part, ml, pre, stats, scores, bytes;
+  size_t smem, part, ml, stats, scores, bytes;
 };
 
 template <typename KT, bool Q32, int HD>
@@ -1070,8 +1164,7 @@ Plan plan_for(const AttnPagedArgs& a, int n_sm) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   p.part = 0;
   p.ml = p.part + up((size_t)p.grid * 2 * p.R * HD * 4);
-  p.pre = p.ml + up((size_t)p.grid * 2 * p.R * 8);
-  p.stats = p.pre + up(4 * (size_t)(a.c.batch + 1));
+  p.stats = p.ml + up((size_t)p.grid * 2 * p.R * 8);
   const size_t most = a.weights ? (size_t)a.c.batch * a.c.Hk * rows : 0;
   p.scores = p.stats + up(most * 8);
   p.bytes = p.scores + up(most * a.c.capacity() * 4);
@@ -1098,7 +1191,6 @@ cudaError_t attn_go(const Launch& L, const AttnPagedArgs& a, int n_sm, void* ws)
   k.scale2 = a.scale * 1.44269504088896340736f;
   k.part = reinterpret_cast<float*>(w + p.part);
   k.ml = reinterpret_cast<float2*>(w + p.ml);
-  k.pre = reinterpret_cast<int*>(w + p.pre);
   k.scores = a.weights ? reinterpret_cast<float*>(w + p.scores) : nullptr;
   k.stats = reinterpret_cast<float2*>(w + p.stats);
   k.grid = p.grid;
@@ -1109,8 +1201,11 @@ cudaError_t attn_go(const Launch& L, const AttnPagedArgs& a, int n_sm, void* ws)
     if (p.cluster) return launch_cluster(L, kernel, p.cluster, dim3(p.grid), dim3(kThreads), p.smem, k);
     return launch_k(L, kernel, dim3(p.grid), dim3(kThreads), p.smem, k);
   });
-  const int joins = p.cluster ? 0 : a.c.Hk * p.rb;
-  const int adds = a.weights ? a.c.Hk * ((a.c.capacity() + kFinishThreads - 1) / kFinishThreads) : 0;
+  // few units: several CTAs join each, so that every load of theirs is under way at once
+  k.slices = 1;
+  while (k.slices < HD / kLeastSlice && (long long)a.c.batch * a.c.Hk * p.rb * k.slices < n_sm) k.slices *= 2;
+  const int joins = p.cluster ? 0 : a.c.Hk * p.rb * k.slices;
+  const int adds = a.weights ? a.c.Hk * ((a.c.capacity() + kWeightTile - 1) / kWeightTile) : 0;
   if (e != cudaSuccess || joins + adds == 0) return e;
   return launch_k(L, attn_finish_kernel<QT>, dim3(joins + adds, a.c.batch), dim3(kFinishThreads), 0, k, p.R, a.weights, a.ldw,
                   bias_of<KT>());
