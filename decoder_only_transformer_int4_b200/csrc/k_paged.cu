@@ -21,10 +21,42 @@ template <> __device__ __forceinline__ float from_f<float>(float x) { return x; 
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// 16 bytes (8 of 16-bit elements made from 4-byte ones) and the values in them, two at a time: one bf16 by the
+// conversion instruction runs at a fraction of the rate of a shift or of the conversion of two (measured on
+// 4132 rows of 48 heads of 128: 32.7 us against fp16's 22.0).
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Pack {
   T e[N];
 };
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Pack<T, N>& p, float (&y)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = to_f<T>(p.e[e]);
+}
+template <int N>
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, N>& p, float (&y)[N]) {
+  const unsigned* w = reinterpret_cast<const unsigned*>(&p);
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    y[e] = __uint_as_float(w[e / 2] << 16);
+    y[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
+  }
+}
+template <int N>
+__device__ __forceinline__ void pack(Pack<float, N>& p, const float (&y)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) p.e[e] = y[e];
+}
+template <int N>
+__device__ __forceinline__ void pack(Pack<__half, N>& p, const float (&y)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) *reinterpret_cast<__half2*>(&p.e[e]) = __floats2half2_rn(y[e], y[e + 1]);
+}
+template <int N>
+__device__ __forceinline__ void pack(Pack<__nv_bfloat16, N>& p, const float (&y)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) *reinterpret_cast<__nv_bfloat162*>(&p.e[e]) = __floats2bfloat162_rn(y[e], y[e + 1]);
+}
 
 }  // namespace
 
@@ -38,59 +70,74 @@ struct alignas(sizeof(T) * N) Pack {
 // the nearest quarter turn (|r| <= 1/8) goes to sincospif in fp32, which is then off by a few
 // 2^-25.  A product in fp32 would be wrong in the second digit at position 10^5.
 //
-// Bound: HBM (every element is read once and written once).  A block takes TOK tokens; their
-// sequence, place and sines are worked out once per token for all heads, then each thread moves
-// the two 16-byte chunks of a pair group per step.
+// Bound: HBM (every element is read once and written once).  A block takes a few tokens; their
+// sequences, places and sines, a chain of three dependent loads and a double-precision reduction, are worked
+// out once for all heads.  A thread then has the same two chunks of 16 bytes in every so-manyth head of its
+// token, so that its sines stay in registers (read from shared memory for each head, their bank conflicts and
+// loads held bf16 rows to half the bandwidth).  32767 rows of 40 heads of 64, fp32 to fp16: 98 us, 6.2 TB/s;
+// 4132 rows of 48 bf16 heads of 128: 25 us, 4.0 TB/s (the chain and the last wave show); 64 rows: 3.2 us.
 // ---------------------------------------------------------------------------------
 namespace {
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kRopeTokens = 8, kRopeItems = 2;
 
 struct TokInfo {
   long long dst;   // element offset of kv head 0's row in the pages, -1: not appended
   int live;
 };
-}  // namespace
 
-template <typename QT, typename KT, int TOK, bool VECTOR>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_paged_kernel(RopeArgs a) {
-  __shared__ float2 cs[TOK][64];
-  __shared__ TokInfo info[TOK];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, t0 = blockIdx.x * TOK;
-  const int nt = min(TOK, a.rows - t0);
-  const int half = a.rot >> 1, hd = a.c.hd, Hk = a.c.Hk;
-  int seq[TOK];
-#pragma unroll
-  for (int k = 0; k < TOK; ++k) seq[k] = 0;
+// Apart, so that neighbouring threads' 16-byte reads of four fall on all banks (as pairs, 4-way conflicts
+// held bf16 rows to half the bandwidth).
+struct alignas(16) Sines {
+  float c[64], s[64];
+};
+
+// Sequence, place and sines of the block's tokens; for all its threads, a barrier at the end.
+__device__ __forceinline__ void rope_tokens(const RopeArgs& a, int t0, int nt, Sines (&cs)[kRopeTokens], TokInfo (&info)[kRopeTokens]) {
+  __shared__ int seq[kRopeTokens];
+  const int tid = threadIdx.x, half = a.rot >> 1;
+  if (tid < kRopeTokens) seq[tid] = 0;
+  __syncthreads();
   // the sequence of token t: how many row_start[i + 1] are <= t
-  for (int i0 = 0; i0 < a.c.batch; i0 += kRopeThreads) {
-    const int i = i0 + tid;
-    const int end = i < a.c.batch ? a.row_start[i + 1] : 0x7fffffff;
+  int mine[kRopeTokens];
 #pragma unroll
-    for (int k = 0; k < TOK; ++k) seq[k] += __syncthreads_count(end <= t0 + k);
+  for (int k = 0; k < kRopeTokens; ++k) mine[k] = 0;
+  for (int i = tid; i < a.c.batch; i += kRopeThreads) {
+    const int end = a.row_start[i + 1];
+#pragma unroll
+    for (int k = 0; k < kRopeTokens; ++k) mine[k] += end <= t0 + k;
   }
-  for (int k = 0; k < nt; ++k) {
+#pragma unroll
+  for (int k = 0; k < kRopeTokens; ++k)
+    if (k < nt) {
+      const int all = __reduce_add_sync(0xffffffffu, mine[k]);
+      if ((tid & 31) == 0 && all) atomicAdd(&seq[k], all);
+    }
+  __syncthreads();
+  for (int it = tid; it < nt * max(half, 1); it += kRopeThreads) {
+    const int k = it / max(half, 1), j = it - k * max(half, 1);
     const int t = t0 + k, b = seq[k];
     const bool live = b < a.c.batch;   // rows behind the last sequence are left as they were
-    int place = 0, pos = 0;
+    int place = 0, r0 = 0, r1 = 0;
     if (live) {
-      const int r0 = a.row_start[b], r1 = a.row_start[b + 1];
+      r0 = a.row_start[b];
+      r1 = a.row_start[b + 1];
       place = a.c.lens[b] - (r1 - r0) + (t - r0);
-      pos = a.positions ? a.positions[t] : place;
-      if (tid == 0) {
-        long long dst = -1;
+    }
+    if (j == 0) {
+      long long dst = -1;
+      if (live) {
         if (t >= r0 && t < r1 && place >= 0 && place < a.c.capacity()) {
           const int page = a.c.table[(size_t)b * a.c.max_pages + (place >> a.c.page_shift)];
           if (page >= 0 && page < a.c.n_pages)
-            dst = page * a.c.page_stride + (long long)(place & (a.c.page() - 1)) * hd;
+            dst = page * a.c.page_stride + (long long)(place & (a.c.page() - 1)) * a.c.hd;
         }
         if (dst < 0) flag_error(a.c.status, kErrShape);
-        info[k].dst = dst;
       }
+      info[k].dst = dst;
+      info[k].live = live;
     }
-    if (tid == 0) info[k].live = live;
-    for (int j = tid; live && j < half; j += kRopeThreads) {
+    if (live && half) {
+      const int pos = a.positions ? a.positions[t] : place;
       const double u = pos * (a.inv_freq[j] * 0.15915494309189533577);   // turns
       const double quarter = rint(4.0 * u);
       float s, c;
@@ -98,122 +145,149 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_paged_kernel(RopeArg
       const int n = (int)((long long)quarter & 3);
       const float cr = n == 0 ? c : n == 1 ? -s : n == 2 ? -c : s;
       const float sr = n == 0 ? s : n == 1 ? c : n == 2 ? -s : -c;
-      cs[k][j] = make_float2(cr * a.mscale, sr * a.mscale);
+      cs[k].c[j] = cr * a.mscale;
+      cs[k].s[j] = sr * a.mscale;
     }
   }
   __syncthreads();
+}
+}  // namespace
 
+namespace {
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = a;
+  a = x * c - b * s;
+  b = x * s + b * c;
+}
+}  // namespace
+
+template <typename QT, typename KT, bool VECTOR>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_paged_kernel(RopeArgs a, int tokens) {
+  __shared__ Sines cs[kRopeTokens];
+  __shared__ TokInfo info[kRopeTokens];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, t0 = blockIdx.x * tokens;
+  const int nt = min(tokens, a.rows - t0);
+  const int half = a.rot >> 1, hd = a.c.hd, Hk = a.c.Hk;
   const int H = a.q ? a.H : 0, heads = H + 2 * Hk;
   KT* const kc = static_cast<KT*>(a.c.k);
   KT* const vc = static_cast<KT*>(a.c.v);
   const long long head_step = (long long)a.c.page() * hd;
+  auto source = [&](int t, int h) {
+    return h < H ? static_cast<const QT*>(a.q) + t * a.ldq + (long long)h * hd
+           : h < H + Hk ? static_cast<const QT*>(a.k) + t * a.ldk + (long long)(h - H) * hd
+                        : static_cast<const QT*>(a.v) + t * a.ldv + (long long)(h - H - Hk) * hd;
+  };
+  auto page_row = [&](int k, int h) {
+    return (h >= H + Hk ? vc + (h - H - Hk) * head_step : kc + (h - H) * head_step) + info[k].dst;
+  };
   if (VECTOR) {
     constexpr int VEC = 16 / sizeof(QT);
     using In = Pack<QT, VEC>;
     using Out = Pack<KT, VEC>;
-    const int per = hd / (2 * VEC);   // pairs of chunks in a head
-    const int items = heads * per, turned = a.rot / (2 * VEC);
-    for (int it = tid; it < nt * items; it += kRopeThreads) {
-      const int k = it / items, rest = it - k * items, h = rest / per, i = rest - h * per;
-      if (!info[k].live) continue;
-      const int t = t0 + k;
-      const bool is_v = h >= H + Hk;
-      int e0, e1;
-      if (a.interleaved || is_v || i >= turned) {
-        e0 = 2 * VEC * i;
-        e1 = e0 + VEC;
-      } else {
-        e0 = VEC * i;
-        e1 = e0 + half;
+    constexpr int U = kRopeItems;
+    // a thread has the same two chunks of every head_groups-th head of one token, and their sines in registers
+    const int shift = hd == 64 ? (VEC == 4 ? 3 : 2) : (VEC == 4 ? 4 : 3);   // 2^shift pairs of chunks in a head
+    const int i = tid & ((1 << shift) - 1), head_groups = (kRopeThreads >> shift) / tokens;   // tokens: a power of two
+    const int slot = tid >> shift, k = slot / head_groups, h0 = slot - k * head_groups;
+    const int turned = a.rot / (2 * VEC);
+    const bool mine = k < nt;
+    // q and k heads: chunks e0, e1; v heads, which pass: f0, f1
+    const int f0 = VEC * i, f1 = f0 + hd / 2;
+    const int e0 = a.interleaved || i < turned ? f0 : a.rot + VEC * (i - turned);
+    const int e1 = a.interleaved ? f1 : e0 + (i < turned ? half : (hd - a.rot) / 2);
+    float c[VEC], s[VEC];
+    int n0 = 0, n1 = 0;   // interleaved: pairs of the two chunks that turn; else of both together
+    rope_tokens(a, t0, nt, cs, info);
+    if (a.interleaved) {
+      n0 = min(max(half - e0 / 2, 0), VEC / 2);
+      n1 = min(max(half - e1 / 2, 0), VEC / 2);
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        c[e] = cs[k].c[e0 / 2 + e];
+        s[e] = cs[k].s[e0 / 2 + e];
+        c[VEC / 2 + e] = cs[k].c[e1 / 2 + e];
+        s[VEC / 2 + e] = cs[k].s[e1 / 2 + e];
       }
-      const QT* src = h < H ? static_cast<const QT*>(a.q) + t * a.ldq + (long long)h * hd
-                    : !is_v ? static_cast<const QT*>(a.k) + t * a.ldk + (long long)(h - H) * hd
-                            : static_cast<const QT*>(a.v) + t * a.ldv + (long long)(h - H - Hk) * hd;
-      const In x0 = *reinterpret_cast<const In*>(src + e0);
-      const In x1 = *reinterpret_cast<const In*>(src + e1);
-      float y0[VEC], y1[VEC];
+    } else if (i < turned) {
+      n0 = VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        y0[e] = to_f<QT>(x0.e[e]);
-        y1[e] = to_f<QT>(x1.e[e]);
+        c[e] = cs[k].c[e0 + e];
+        s[e] = cs[k].s[e0 + e];
       }
-      if (!is_v) {
-        if (a.interleaved) {
+    }
+    if (!mine || !info[k].live) return;
+    for (int h1 = h0; h1 < heads; h1 += U * head_groups) {
+      In x0[U], x1[U];
 #pragma unroll
-          for (int e = 0; e < VEC; e += 2) {
-            const int j0 = (e0 + e) >> 1, j1 = (e1 + e) >> 1;
-            if (j0 < half) {
-              const float2 w = cs[k][j0];
-              const float p = y0[e], c = y0[e + 1];
-              y0[e] = p * w.x - c * w.y;
-              y0[e + 1] = p * w.y + c * w.x;
-            }
-            if (j1 < half) {
-              const float2 w = cs[k][j1];
-              const float p = y1[e], c = y1[e + 1];
-              y1[e] = p * w.x - c * w.y;
-              y1[e + 1] = p * w.y + c * w.x;
-            }
-          }
-        } else if (i < turned) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float2 w = cs[k][e0 + e];
-            const float p = y0[e], c = y1[e];
-            y0[e] = p * w.x - c * w.y;
-            y1[e] = p * w.y + c * w.x;
-          }
+      for (int u = 0; u < U; ++u) {
+        const int h = h1 + u * head_groups;
+        if (h < heads) {
+          const QT* src = source(t0 + k, h);
+          x0[u] = *reinterpret_cast<const In*>(src + (h < H + Hk ? e0 : f0));
+          x1[u] = *reinterpret_cast<const In*>(src + (h < H + Hk ? e1 : f1));
         }
       }
-      if (h < H) {
-        QT* dst = static_cast<QT*>(a.q_out) + t * a.ldo + (long long)h * hd;
-        In z0, z1;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          z0.e[e] = from_f<QT>(y0[e]);
-          z1.e[e] = from_f<QT>(y1[e]);
-        }
-        *reinterpret_cast<In*>(dst + e0) = z0;
-        *reinterpret_cast<In*>(dst + e1) = z1;
-      } else if (info[k].dst >= 0) {
-        KT* dst = (is_v ? vc + (h - H - Hk) * head_step : kc + (h - H) * head_step) + info[k].dst;
-        Out z0, z1;
+      for (int u = 0; u < U; ++u) {
+        const int h = h1 + u * head_groups;
+        if (h < heads) {
+          const bool is_v = h >= H + Hk;
+          float y0[VEC], y1[VEC];
+          unpack(x0[u], y0);
+          unpack(x1[u], y1);
+          if (!is_v) {
+            if (a.interleaved) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          z0.e[e] = from_f<KT>(y0[e]);
-          z1.e[e] = from_f<KT>(y1[e]);
+              for (int e = 0; e < VEC / 2; ++e) {
+                if (e < n0) turn(y0[2 * e], y0[2 * e + 1], c[e], s[e]);
+                if (e < n1) turn(y1[2 * e], y1[2 * e + 1], c[VEC / 2 + e], s[VEC / 2 + e]);
+              }
+            } else if (n0) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) turn(y0[e], y1[e], c[e], s[e]);
+            }
+          }
+          if (h < H) {
+            QT* dst = static_cast<QT*>(a.q_out) + (t0 + k) * a.ldo + (long long)h * hd;
+            In z0, z1;
+            pack(z0, y0);
+            pack(z1, y1);
+            *reinterpret_cast<In*>(dst + e0) = z0;
+            *reinterpret_cast<In*>(dst + e1) = z1;
+          } else if (info[k].dst >= 0) {
+            KT* dst = page_row(k, h);
+            Out z0, z1;
+            pack(z0, y0);
+            pack(z1, y1);
+            *reinterpret_cast<Out*>(dst + (is_v ? f0 : e0)) = z0;
+            *reinterpret_cast<Out*>(dst + (is_v ? f1 : e1)) = z1;
+          }
         }
-        *reinterpret_cast<Out*>(dst + e0) = z0;
-        *reinterpret_cast<Out*>(dst + e1) = z1;
       }
     }
   } else {
     // odd strides, unaligned rows or half-layout pairs that do not fall on chunks: a thread moves
     // the two elements of a pair (of two passing elements) at a time
+    rope_tokens(a, t0, nt, cs, info);
     const int per = hd / 2, items = heads * per;
     for (int it = tid; it < nt * items; it += kRopeThreads) {
       const int k = it / items, rest = it - k * items, h = rest / per, i = rest - h * per;
       if (!info[k].live) continue;
-      const int t = t0 + k;
-      const bool is_v = h >= H + Hk, turn = !is_v && i < half;
-      const int e0 = turn && !a.interleaved ? i : 2 * i;
-      const int e1 = turn && !a.interleaved ? i + half : 2 * i + 1;
-      const QT* src = h < H ? static_cast<const QT*>(a.q) + t * a.ldq + (long long)h * hd
-                    : !is_v ? static_cast<const QT*>(a.k) + t * a.ldk + (long long)(h - H) * hd
-                            : static_cast<const QT*>(a.v) + t * a.ldv + (long long)(h - H - Hk) * hd;
+      const bool turned = h < H + Hk && i < half;
+      const int e0 = turned && !a.interleaved ? i : 2 * i;
+      const int e1 = turned && !a.interleaved ? i + half : 2 * i + 1;
+      const QT* src = source(t0 + k, h);
       float y0 = to_f<QT>(src[e0]), y1 = to_f<QT>(src[e1]);
-      if (turn) {
-        const float2 w = cs[k][i];
-        const float p = y0, c = y1;
-        y0 = p * w.x - c * w.y;
-        y1 = p * w.y + c * w.x;
-      }
+      if (turned) turn(y0, y1, cs[k].c[i], cs[k].s[i]);
       if (h < H) {
-        QT* dst = static_cast<QT*>(a.q_out) + t * a.ldo + (long long)h * hd;
+        QT* dst = static_cast<QT*>(a.q_out) + (t0 + k) * a.ldo + (long long)h * hd;
         dst[e0] = from_f<QT>(y0);
         dst[e1] = from_f<QT>(y1);
       } else if (info[k].dst >= 0) {
-        KT* dst = (is_v ? vc + (h - H - Hk) * head_step : kc + (h - H) * head_step) + info[k].dst;
+        KT* dst = page_row(k, h);
         dst[e0] = from_f<KT>(y0);
         dst[e1] = from_f<KT>(y1);
       }
@@ -228,15 +302,13 @@ static cudaError_t rope_go(const Launch& L, const RopeArgs& a) {
   // 16-byte accesses need aligned rows, and half-layout pairs that fall on whole chunks
   const bool vector = !off(a.q, a.ldq) && !off(a.k, a.ldk) && !off(a.v, a.ldv) && !off(a.q ? a.q_out : nullptr, a.ldo) &&
                       (a.interleaved || a.rot % (2 * VEC) == 0);
-  constexpr int kMany = 4;
-  const bool many = a.rows >= 148 * 8 * kMany;
-  const dim3 block(kRopeThreads);
-  if (vector) {
-    if (many) return launch_k(L, rope_append_paged_kernel<QT, KT, kMany, true>, dim3((a.rows + kMany - 1) / kMany), block, 0, a);
-    return launch_k(L, rope_append_paged_kernel<QT, KT, 1, true>, dim3(a.rows), block, 0, a);
-  }
-  if (many) return launch_k(L, rope_append_paged_kernel<QT, KT, kMany, false>, dim3((a.rows + kMany - 1) / kMany), block, 0, a);
-  return launch_k(L, rope_append_paged_kernel<QT, KT, 1, false>, dim3(a.rows), block, 0, a);
+  // Tokens a block, a power of two: more of them share the chain, but 1.5 waves of blocks have to be left to
+  // overlap one block's chain with another's copies (4132 rows: 26.7 us at 8, 25.2 at 4; 32767: 98 at 8, 103 at 4)
+  int tokens = 1;
+  while (tokens < kRopeTokens && a.rows >= 148 * 6 * 2 * tokens) tokens *= 2;
+  const dim3 grid((a.rows + tokens - 1) / tokens), block(kRopeThreads);
+  if (vector) return launch_k(L, rope_append_paged_kernel<QT, KT, true>, grid, block, 0, a, tokens);
+  return launch_k(L, rope_append_paged_kernel<QT, KT, false>, grid, block, 0, a, tokens);
 }
 
 cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_elem) {
