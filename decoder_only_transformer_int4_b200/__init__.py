@@ -294,15 +294,24 @@ class PagedKV:
     """One layer's paged cache (ms_paged_kv): K and V pages [n_pages, kv_heads, page_size, head_dim] (the
     first dimension may be strided), table int32 [batch, max_pages], lens int32 [batch] with the rows of
     the next call included; status (optional): int32 [1], zeroed, collects errors in device data (op_status).
-    Holds the tensors; writes to them in place are seen by later calls.  The attributes are only read: other
-    tensors need another PagedKV."""
+    Holds the tensors; writes to them in place are seen by later calls."""
 
-    __slots__ = ("k", "v", "table", "lens", "status", "_h", "n_kv_heads", "head_dim", "capacity", "batch")
+    __slots__ = ("_h", "_sizes", "_tensors")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                  status: Optional[torch.Tensor] = None):
-        self._h, self.n_kv_heads, self.head_dim, self.capacity, self.batch = _paged.kv(k, v, table, lens, status)
-        self.k, self.v, self.table, self.lens, self.status = k, v, table, lens, status
+        self._h, *self._sizes = _paged.kv(k, v, table, lens, status)
+        self._tensors = (k, v, table, lens, status)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    table = property(lambda self: self._tensors[2])
+    lens = property(lambda self: self._tensors[3])
+    status = property(lambda self: self._tensors[4])
+    n_kv_heads = property(lambda self: self._sizes[0])
+    head_dim = property(lambda self: self._sizes[1])
+    capacity = property(lambda self: self._sizes[2], doc="positions that a sequence's row of the table holds")
+    batch = property(lambda self: self._sizes[3])
 
 
 def rope_append_paged(kv: PagedKV, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,

@@ -151,7 +151,15 @@ __global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a,
     }
     return;
   }
-  const double goal = (double)a.u_sample[b] * total;
+  const float u = a.u_sample[b];
+  if (!(u >= 0.f && u < 1.f)) {
+    if (rank == 0 && tid == 0) {
+      out[taken] = -1;
+      flag_error(status, kErrToken);
+    }
+    return;
+  }
+  const double goal = (double)u * total;
   double at = __shfl_up_sync(0xffffffffu, incl, 1);
   if (lane == 0) at = 0.0;
   // the last run that begins at or below the goal and has any weight

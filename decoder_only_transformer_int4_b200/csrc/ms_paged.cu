@@ -113,7 +113,7 @@ ms_status ms_op_status(uint32_t* status, void* stream) {
   if (bits & ms::kErrShapeBit)
     return bad(MS_ERR_SHAPE, "ms_op_status", "a length, row range or page was out of its limits");
   if (bits & ms::kErrTokenBit)
-    return bad(MS_ERR_TOKEN_RANGE, "ms_op_status", "a token was out of range, or probabilities summed to nothing");
+    return bad(MS_ERR_TOKEN_RANGE, "ms_op_status", "a token or random number was out of range, or probabilities summed to nothing");
   return MS_OK;
 }
 

@@ -93,12 +93,11 @@ float float_arg(PyObject* o) {
   return static_cast<float>(v);
 }
 
-// The cache's description with what keeps its device; the tensors are held by the Python object.
+// The cache's description, its device and the tensors that it points into.
 struct Kv {
   ms_paged_kv s;
   at::Device dev;
-  at::ScalarType type;
-  int64_t capacity() const { return (int64_t)s.max_pages * s.page_size; }
+  at::Tensor held[5];
 };
 constexpr const char* kKvName = "ms_paged_kv";
 void free_kv(PyObject* o) { delete static_cast<Kv*>(PyCapsule_GetPointer(o, kKvName)); }
@@ -140,7 +139,7 @@ PyObject* py_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     refuse("k and v", "the elements of a page must lie together");
   if (table.dim() != 2) refuse("table", "expected [batch, max_pages]");
   const int64_t batch = table.size(0), most = table.size(1);
-  std::unique_ptr<Kv> kv(new Kv{{}, dev, k.scalar_type()});
+  std::unique_ptr<Kv> kv(new Kv{{}, dev, {k, v, table, lens}});
   kv->s.k = k.data_ptr();
   kv->s.v = v.data_ptr();
   kv->s.elem = elem(k, "k");
@@ -154,6 +153,7 @@ PyObject* py_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   kv->s.batch = as_int(batch, "table");
   kv->s.lens = static_cast<const int32_t*>(flat(lens, "lens", at::kInt, {batch}, dev));
   kv->s.status = none(a[4]) ? nullptr : static_cast<uint32_t*>(flat(tensor(a[4], "status"), "status", at::kInt, {1}, dev));
+  if (!none(a[4])) kv->held[4] = tensor(a[4], "status");
   THPObjectPtr cap(PyCapsule_New(kv.get(), kKvName, free_kv));
   if (!cap) throw python_error();
   kv.release();

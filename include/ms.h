@@ -379,8 +379,8 @@ typedef struct {
 
 /* Synchronises `stream`, reads and clears a status word of these operators (uint32, zeroed by the
  * caller before first use) and returns MS_ERR_SHAPE (a length, row range or page out of its
- * limits), MS_ERR_TOKEN_RANGE (a token out of range, or probabilities that sum to nothing) or
- * MS_OK. */
+ * limits), MS_ERR_TOKEN_RANGE (a token or random number out of range, or probabilities that sum to
+ * nothing) or MS_OK. */
 ms_status ms_op_status(uint32_t* status, void* stream);
 
 /* Rotary positions of new q and k rows and the append of k and v to the cache.
@@ -414,7 +414,8 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
  * h / (n_heads / n_kv_heads):
  *     out = sum_t p_t v_t,   p = softmax_t(scale * q . k_t).
  * A row that sees no position (T = 0, or n > T) gives 0.  What lies behind a sequence's end, or a row's last visible
- * position, never enters, whatever the memory holds.  n <= max_rows (1 .. 64): one row is decoding,
+ * position, never enters, whatever the memory holds; a k or v that is not finite makes the rows that see it so
+ * (fp32: of magnitude below 2^127).  n <= max_rows (1 .. 64): one row is decoding,
  * several are drafts.  q and out [rows][n_heads][head_dim] of q_elem at strides ldq, ldo; rows behind
  * row_start[batch] are left as they were.
  * weights (may be NULL): fp32 [batch][n_kv_heads][ldw], ldw >= max_pages * page_size: position t's entry
@@ -457,8 +458,8 @@ ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t
  * u_sample[b] times the total.  Products and sums in double.
  * accepted int32 [batch]; out int32 [batch][max_draft + 1]: the accepted drafts, the next token, -1 behind.
  * Probabilities are finite and not negative (they need not sum to 1), random numbers in [0, 1).  A token outside
- * [0, vocab) is refused, a row that sums to nothing gives the next token -1; both flag status
- * (may be NULL), as does a row range out of its limits (nothing accepted, every token -1). */
+ * [0, vocab) is refused, a row that sums to nothing (or not to a finite number) or a u_sample outside [0, 1) gives the
+ * next token -1; all flag status (may be NULL), as does a row range out of its limits (nothing accepted, every token -1). */
 ms_status ms_op_verify_draft(const float* target, int64_t ld_target, const float* draft, int64_t ld_draft,
                              const int32_t* tokens, const int32_t* row_start, int rows, int batch, int max_draft,
                              int vocab, const float* u_accept, const float* u_sample, int32_t* accepted,
