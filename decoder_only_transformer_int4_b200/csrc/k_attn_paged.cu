@@ -93,7 +93,8 @@ struct Shape {
   static constexpr int kQBytes = R * HD * ((kF32 || Q32) ? 4 : 2);   // Q32 on halves: hi and lo planes
   static constexpr bool kQRegs = !kF32 && NB * (HD / 16) * (Q32 ? 2 : 1) <= 16;   // Q's fragments stay in registers
   static constexpr int kObufStride = HD + 4;
-  static constexpr int kObufBytes = R * kObufStride * 4;
+  static constexpr int kBufs = HD == 64 && NB <= 2 ? kWarps : 1;   // buffers of the merge: one a warp, or one in turn
+  static constexpr int kObufBytes = kBufs * R * kObufStride * 4;
   static constexpr int kDescBytes = kWarps * kRing * (int)sizeof(Desc);
   static constexpr int kSmall = R * 4 * (2 + 2 * kWarps + 2);
   static constexpr int kFixed = kWarps * kStages * kStageBytes + kQBytes + kObufBytes + kDescBytes + kSmall;
@@ -389,7 +390,25 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     ldsm4(t, smem_u32(qs) + (plane * R * HD + r * HD + ((c ^ (r & 7)) << 3)) * 2);
   };
 
+  // A unit's sequence and query rows (one warp, every fourth row), read before they are needed: ahead of the first
+  // copies of K and V, which would hold them up, and for a later unit ahead of the merge of the one before.
+  constexpr int kQRows = R / kWarps;
+  constexpr bool kEarly = NB <= 2;   // else the registers are full until the merge is done
+  float xq[kQRows][HD / 32];
+  int next_r0 = 0, next_n = 0, next_T = 0;
+  auto fetch_rows = [&](const Desc& e) {
+    seq_info(a, e.b, next_r0, next_n, next_T, false);
+#pragma unroll
+    for (int j = 0; j < kQRows; ++j) {
+      const int rr = e.row0 + warp + j * kWarps, i = rr / a.hpg, h = rr - i * a.hpg;
+      const QT* src = static_cast<const QT*>(a.q) + (next_r0 + (i < next_n ? i : 0)) * a.ldq + (long long)(e.kvh * a.hpg + h) * HD;
+#pragma unroll
+      for (int k = 0; k < HD / 32; ++k) xq[j][k] = i < next_n ? as_float<QT>(src[k * 32 + lane]) : 0.f;
+    }
+  };
+
   look_up(0);
+  if (niter > 0) fetch_rows(my[0]);
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
     if (s < niter) issue(s);
@@ -423,17 +442,10 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     if (d.ends & 1) {
       begins_unit = d.ends & 2;
       __syncthreads();   // the previous unit's rows and sums are no longer read
-      seq_info(a, d.b, seq_r0, seq_n, seq_T, false);
+      seq_r0 = next_r0;
+      seq_n = next_n;
+      seq_T = next_T;
       least = seq_T - seq_n + 1;   // positions that every row of the sequence sees
-      constexpr int kQRows = R / kWarps;
-      float xq[kQRows][HD / 32];
-#pragma unroll
-      for (int j = 0; j < kQRows; ++j) {   // all loads first
-        const int rr = tile_row + warp + j * kWarps, i = rr / a.hpg, h = rr - i * a.hpg;
-        const QT* src = static_cast<const QT*>(a.q) + (seq_r0 + (i < seq_n ? i : 0)) * a.ldq + (long long)(kvh * a.hpg + h) * HD;
-#pragma unroll
-        for (int k = 0; k < HD / 32; ++k) xq[j][k] = i < seq_n ? as_float<QT>(src[k * 32 + lane]) : 0.f;
-      }
 #pragma unroll
       for (int j = 0; j < kQRows; ++j) {
         const int r = warp + j * kWarps, i = (tile_row + r) / a.hpg;
@@ -767,6 +779,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
     __syncwarp();   // the ring's next copy goes into this stage
 
     if (d.ends & 4) {
+      if (kEarly && it + 1 < niter) fetch_rows(my[(it + 1) & (kRing - 1)]);
       // the four warps' references and sums, then their weighted sums of V, one warp after the other
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -802,35 +815,53 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
           const float top = mf[nb * 8 + 2 * t4 + k];
           scale[nb][k] = ex2(m[nb][k] - (top == -INFINITY ? 0.f : top));
         }
-#pragma unroll 1
-      for (int round = 0; round < kWarps; ++round) {
-        if (warp == round) {
+      if constexpr (S::kBufs > 1) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float* const rows = obuf + (nb * 8 + 2 * t4) * S::kObufStride;
-            float was[MD][4];   // all loads of a row tile before its stores
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int md = 0; md < MD; ++md)
+          for (int md = 0; md < MD; ++md)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) was[md][k] = round ? rows[(k & 1) * S::kObufStride + dim_of(md, k)] : 0.f;
-#pragma unroll
-            for (int md = 0; md < MD; ++md)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                rows[(k & 1) * S::kObufStride + dim_of(md, k)] = fmaf(O[nb][md][k], scale[nb][k & 1], was[md][k]);
-          }
-        }
+            for (int k = 0; k < 4; ++k)
+              obuf[(warp * R + nb * 8 + 2 * t4 + (k & 1)) * S::kObufStride + dim_of(md, k)] = O[nb][md][k] * scale[nb][k & 1];
         __syncthreads();
+      } else {
+#pragma unroll 1
+        for (int round = 0; round < kWarps; ++round) {
+          if (warp == round) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              float* const rows = obuf + (nb * 8 + 2 * t4) * S::kObufStride;
+              float was[MD][4];   // all loads of a row tile before its stores
+#pragma unroll
+              for (int md = 0; md < MD; ++md)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) was[md][k] = round ? rows[(k & 1) * S::kObufStride + dim_of(md, k)] : 0.f;
+#pragma unroll
+              for (int md = 0; md < MD; ++md)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  rows[(k & 1) * S::kObufStride + dim_of(md, k)] = fmaf(O[nb][md][k], scale[nb][k & 1], was[md][k]);
+            }
+          }
+          __syncthreads();
+        }
       }
+      auto merged = [&](int r, int e) {
+        float o = obuf[r * S::kObufStride + e];
+#pragma unroll
+        for (int w = 1; w < S::kBufs; ++w) o += obuf[(w * R + r) * S::kObufStride + e];
+        return o;
+      };
       const int real = min(R, seq_n * a.hpg - tile_row);
-      if (a.cluster) {
-        // joined below
+      if (a.cluster) {   // joined below
+        if constexpr (S::kBufs > 1)
+          for (int i = tid; i < R * HD; i += kThreads) obuf[i / HD * S::kObufStride + i % HD] = merged(i / HD, i % HD);
       } else if (begins_unit && (d.ends & 8)) {
         QT* dst = static_cast<QT*>(a.out);
         for (int i = tid; i < real * HD; i += kThreads) {
           const int r = i / HD, e = i - r * HD;
           const int rr = tile_row + r, row = rr / a.hpg, h = rr - row * a.hpg;
-          const float o = obuf[r * S::kObufStride + e];
+          const float o = merged(r, e);
           dst[(seq_r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * HD + e] = rounded<QT>(finish(o, lf[r], slim[r]));
         }
         if (a.scores && tid < real)
@@ -839,10 +870,11 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
         const long long slot = (long long)blockIdx.x * 2 + (begins_unit ? 1 : 0);
         for (int i = tid; i < real * HD; i += kThreads) {
           const int r = i / HD, e = i - r * HD;
-          a.part[(slot * R + r) * HD + e] = obuf[r * S::kObufStride + e];
+          a.part[(slot * R + r) * HD + e] = merged(r, e);
         }
         if (tid < real) a.ml[slot * R + tid] = make_float2(mf[tid], lf[tid]);
       }
+      if (!kEarly && it + 1 < niter) fetch_rows(my[(it + 1) & (kRing - 1)]);
     }
   }
 
