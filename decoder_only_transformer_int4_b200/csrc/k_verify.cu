@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a,
   pdl_wait();
   pdl_trigger();
   const int r0 = a.row_start[b];
+  const float u = a.u_sample[b];
   int n = a.row_start[b + 1] - r0;
   const bool ok = n >= 0 && n <= a.max_draft && r0 >= 0 && r0 + (long long)n <= a.rows;
   if (!ok) n = 0;   // flagged below; every CTA of the cluster takes the same way out
@@ -151,7 +152,6 @@ __global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a,
     }
     return;
   }
-  const float u = a.u_sample[b];
   if (!(u >= 0.f && u < 1.f)) {
     if (rank == 0 && tid == 0) {
       out[taken] = -1;
