@@ -529,13 +529,16 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
       // lo: the products with a lo half, where the result is stored in fp32.  They are summed apart, since
       // the tensor cores cut an addition's result off: fewer cuts fall on the large sum.
       constexpr bool kApart = F32 || Q32;
-      float sc[NB][4], lo[kApart ? NB : 1][4];
+      // Few row tiles: a second sum for every other product, so that none waits for the one before it.
+      constexpr bool kTwoSums = !F32 && NB <= 2;
+      float sc[NB][4], lo[kApart ? NB : 1][4], sd[kTwoSums ? NB : 1][4];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           sc[nb][k] = 0.f;
           if constexpr (kApart) lo[nb][k] = 0.f;
+          if constexpr (kTwoSums) sd[nb][k] = 0.f;
         }
 
       // S^T = K Q^T
@@ -548,23 +551,31 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
             const int r = lane & 15, c = 2 * (ks + u) + (lane >> 4);
             ldsm4(ka[u], ku + r * S::kRowBytes + swz_k<false>(c, r) * 16);
           }
+          uint32_t t[S::kQRegs ? 1 : NB][4];
+          if constexpr (!S::kQRegs) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            uint32_t t[4];
-            if constexpr (!S::kQRegs) load_q(t, nb, ks, 0);
+            for (int nb = 0; nb < NB; ++nb) load_q(t[nb], nb, ks, 0);
+          }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if constexpr (S::kQRegs) mma16<KT>(sc[nb], ka[u], qreg[nb][ks + u][0], qreg[nb][ks + u][1]);
-              else mma16<KT>(sc[nb], ka[u], t[2 * u], t[2 * u + 1]);
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              float(&sum)[4] = kTwoSums && u ? sd[kTwoSums ? nb : 0] : sc[nb];
+              if constexpr (S::kQRegs) mma16<KT>(sum, ka[u], qreg[nb][ks + u][0], qreg[nb][ks + u][1]);
+              else mma16<KT>(sum, ka[u], t[nb][2 * u], t[nb][2 * u + 1]);
             }
-            if constexpr (Q32) {
-              if constexpr (!S::kQRegs) load_q(t, nb, ks, 1);
+          if constexpr (Q32) {
+            if constexpr (!S::kQRegs) {
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
+              for (int nb = 0; nb < NB; ++nb) load_q(t[nb], nb, ks, 1);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
                 if constexpr (S::kQRegs) mma16<KT>(lo[nb], ka[u], qreg[nb][ks + u][2], qreg[nb][ks + u][3]);
-                else mma16<KT>(lo[nb], ka[u], t[2 * u], t[2 * u + 1]);
+                else mma16<KT>(lo[nb], ka[u], t[nb][2 * u], t[nb][2 * u + 1]);
               }
-            }
           }
         }
       } else {
@@ -609,6 +620,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float s = sc[nb][k];
+          if constexpr (kTwoSums) s += sd[nb][k];
           if constexpr (kApart) s += lo[nb][k];
           sc[nb][k] = s * fac[nb][k & 1];
         }
@@ -706,23 +718,44 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
             ph[nb][i] = transpose8(h);   // positions 2 t4, 2 t4 + 1 (+ 8 i) of row g8: a B fragment
             pl[nb][i] = transpose8(w);
           }
+        // two tiles of elements at a time: products that add to one sum stay 2 NB apart
 #pragma unroll
-        for (int md = 0; md < MD; ++md) {
-          uint32_t va[4];
-          const int r = (lane & 7) + 8 * (lane >> 4), c = 2 * md + ((lane >> 3) & 1);
-          ldsm4t(va, vu + r * S::kRowBytes + swz_v<false>(c, r) * 16);
+        for (int md = 0; md < MD; md += 2) {
+          uint32_t va[2][4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            if constexpr (Q32) {
-              float x[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16<KT>(x, va, pl[nb][0], pl[nb][1]);
-              mma16<KT>(x, va, ph[nb][0], ph[nb][1]);
+          for (int u = 0; u < 2; ++u) {
+            const int r = (lane & 7) + 8 * (lane >> 4), c = 2 * (md + u) + ((lane >> 3) & 1);
+            ldsm4t(va[u], vu + r * S::kRowBytes + swz_v<false>(c, r) * 16);
+          }
+          if constexpr (Q32) {
+            float x[2][NB][4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) O[nb][md][k] += x[k];
-            } else {
-              mma16<KT>(O[nb][md], va, ph[nb][0], ph[nb][1]);
-              mma16<KT>(O[nb][md], va, pl[nb][0], pl[nb][1]);
-            }
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[u][nb][k] = 0.f;
+                mma16<KT>(x[u][nb], va[u], pl[nb][0], pl[nb][1]);
+              }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<KT>(x[u][nb], va[u], ph[nb][0], ph[nb][1]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) O[nb][md + u][k] += x[u][nb][k];
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<KT>(O[nb][md + u], va[u], ph[nb][0], ph[nb][1]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<KT>(O[nb][md + u], va[u], pl[nb][0], pl[nb][1]);
           }
         }
       } else {
