@@ -389,12 +389,14 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a,
   const int runs = C * kEvWarps, run = rank * kEvWarps + warp;
   const int kn = (T + 32 * runs - 1) / (32 * runs);
   const int i0 = run * kn * 32 + lane;   // below 2 (T + 32 runs) < 2^31
-  for (int k0 = 0; k0 < min(kn, kEvHeld); k0 += 4) {
-    float x[4];
+  constexpr int kAtOnce = 10;
+  static_assert(kEvHeld % kAtOnce == 0, "");
+  for (int k0 = 0; k0 < min(kn, kEvHeld); k0 += kAtOnce) {
+    float x[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = weight(i0 + 32 * (k0 + k));
+    for (int k = 0; k < kAtOnce; ++k) x[k] = weight(i0 + 32 * (k0 + k));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) held[k0 + k][tid] = key_of(i0 + 32 * (k0 + k), x[k]);   // read by this thread alone
+    for (int k = 0; k < kAtOnce; ++k) held[k0 + k][tid] = key_of(i0 + 32 * (k0 + k), x[k]);   // read by this thread alone
   }
   auto each = [&](auto&& f) {
 #pragma unroll 4
