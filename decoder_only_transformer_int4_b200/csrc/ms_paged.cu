@@ -20,6 +20,9 @@ ms_status bad(ms_status s, const char* who, const char* what) {
 ms_status done(cudaError_t e, const char* who) { return e == cudaSuccess ? MS_OK : bad(MS_ERR_CUDA, who, cudaGetErrorString(e)); }
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// every int32 or fp32 array among the arguments (null ones are checked apart)
+template <typename... Ptr>
+bool aligned4(Ptr... p) { return (aligned(p, 4) && ...); }
 size_t elem_bytes(int e) { return e == MS_ELEM_F32 ? 4 : 2; }
 
 // MS_OK, or the reason why the cache cannot be used.
@@ -38,6 +41,7 @@ ms_status check_kv(const ms_paged_kv* kv, const char* who) {
   const long long page = (long long)kv->n_kv_heads * kv->page_size * kv->head_dim;
   if (kv->page_stride < page || kv->page_stride > (1ll << 40) || kv->page_stride * (long long)elem_bytes(kv->elem) % 16)
     return bad(MS_ERR_SHAPE, who, "page_stride must hold a page and be a multiple of 16 bytes");
+  if (!aligned4(kv->table, kv->lens, kv->status)) return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
   if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return bad(MS_ERR_INVALID_ARG, who, "the pages must be 16-byte aligned");
   return MS_OK;
 }
@@ -103,7 +107,7 @@ ms::AttnPagedArgs attn_args(const ms_paged_kv& kv, int n_heads, int max_rows, fl
 extern "C" {
 
 ms_status ms_op_status(uint32_t* status, void* stream) {
-  if (!status) return bad(MS_ERR_INVALID_ARG, "ms_op_status", "null status word");
+  if (!status || !aligned4(status)) return bad(MS_ERR_INVALID_ARG, "ms_op_status", "null or unaligned status word");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint32_t bits = 0;
   cudaError_t e = cudaMemcpyAsync(&bits, status, sizeof(bits), cudaMemcpyDeviceToHost, st);
@@ -138,7 +142,7 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
   if (ldk < kw || ldv < kw || (q && (ldq < qw || ldq_out < qw)) || ldk > most || ldv > most || (q && (ldq > most || ldq_out > most)))
     return bad(MS_ERR_SHAPE, who, "a row stride is smaller than its row");
   const size_t eb = elem_bytes(q_elem);
-  if (!aligned(k, eb) || !aligned(v, eb) || !aligned(q, eb) || !aligned(q_out, eb) || !aligned(inv_freq, 8))
+  if (!aligned(k, eb) || !aligned(v, eb) || !aligned(q, eb) || !aligned(q_out, eb) || !aligned(inv_freq, 8) || !aligned4(row_start, positions))
     return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
   if (rows == 0) return MS_OK;
   ms::RopeArgs a{view(*kv), q,       k,          v,         ldq,                 ldk,    ldv,      ldq_out,   q_out,
@@ -174,7 +178,7 @@ ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, in
   if (weights && (ldw < (int64_t)kv->max_pages * kv->page_size || ldw > most))
     return bad(MS_ERR_SHAPE, who, "ldw must hold max_pages * page_size positions");
   const size_t eb = elem_bytes(q_elem);
-  if (!aligned(q, eb) || !aligned(out, eb) || !aligned(weights, 4))
+  if (!aligned(q, eb) || !aligned(out, eb) || !aligned4(weights, row_start))
     return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
   if (!aligned(workspace, 256)) return bad(MS_ERR_INVALID_ARG, who, "the workspace must be 256-byte aligned");
   int n_sm = 0;
@@ -202,6 +206,7 @@ ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t
   const ms_status s = check_kv(kv, who);
   if (s != MS_OK) return s;
   if (!weights || !dst_table || !kept || !weights_out || !lens_out) return bad(MS_ERR_INVALID_ARG, who, "null pointer");
+  if (!aligned4(weights, dst_table, kept, weights_out, lens_out)) return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
   if (lens_out == kv->lens) return bad(MS_ERR_INVALID_ARG, who, "lens_out must not be the cache's lens");
   if (keep < 1 || first < 0 || recent < 0 || (int64_t)first + recent > keep)
     return bad(MS_ERR_SHAPE, who, "need keep >= 1, first, recent >= 0 and first + recent <= keep");
@@ -224,6 +229,8 @@ ms_status ms_op_verify_draft(const float* target, int64_t ld_target, const float
   if (rows < 0 || batch < 1 || batch > (1 << 20) || vocab < 1 || max_draft < 0 || max_draft > 256)
     return bad(MS_ERR_SHAPE, who, "need rows >= 0, 1 <= batch <= 2^20, vocab >= 1 and 0 <= max_draft <= 256");
   if (rows > 0 && max_draft > 0 && (!tokens || !u_accept)) return bad(MS_ERR_INVALID_ARG, who, "null pointer");
+  if (!aligned4(target, draft, tokens, row_start, u_accept, u_sample, accepted, out, status))
+    return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
   if (ld_target < vocab || (draft && ld_draft < vocab) || ld_target > (1ll << 40) || ld_draft > (1ll << 40))
     return bad(MS_ERR_SHAPE, who, "a row stride is smaller than the vocabulary");
   ms::VerifyArgs a{target, draft, ld_target, ld_draft, tokens, row_start, rows, batch, max_draft, vocab, u_accept, u_sample, accepted, out};

@@ -416,7 +416,7 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
  * A row that sees no position (T = 0, or n > T) gives 0.  What lies behind a sequence's end, or a row's last visible
  * position, never enters, whatever the memory holds; a k or v that is not finite makes the rows that see it so
  * (fp32: of magnitude below 2^127).  n <= max_rows (1 .. 64): one row is decoding,
- * several are drafts.  q and out [rows][n_heads][head_dim] of q_elem at strides ldq, ldo; rows behind
+ * several are drafts.  out may be q.  q and out [rows][n_heads][head_dim] of q_elem at strides ldq, ldo; rows behind
  * row_start[batch] are left as they were.
  * weights (may be NULL): fp32 [batch][n_kv_heads][ldw], ldw >= max_pages * page_size: position t's entry
  * grows by the sum of p_t over the rows and the heads of its group (for ms_op_evict_paged).
@@ -424,7 +424,7 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
  * of 11-bit halves, probabilities as pairs of 16-bit halves); rounded once at the store.  The
  * result of a sequence does not depend on timing, but its rounding on how the batch's work is split.
  * workspace: ms_op_attn_paged_workspace bytes (0 for arguments that the call refuses), 256-byte
- * aligned, holding nothing before or after; calls that may overlap on the GPU need their own.
+ * aligned, holding nothing before or after; calls that may overlap on the GPU need their own, and their own weights.
  * max_pages * page_size < 2^30. */
 size_t ms_op_attn_paged_workspace(const ms_paged_kv* kv, int q_elem, int n_heads, int max_rows, int with_weights);
 ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, int q_elem, int rows, int max_rows,
@@ -442,7 +442,7 @@ ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, in
  * weights in the new order and 0 behind; weights_out may be weights (with ldw_out = ldw), else
  * they must not overlap.  ldw >= max_pages * page_size, ldw_out >= keep.
  * kept int32 [batch][n_kv_heads][keep]: the old positions, -1 behind.  lens_out int32 [batch]:
- * min(lens, keep); not kv->lens itself.  first, recent >= 0, first + recent <= keep, keep >= 1. */
+ * min(lens, keep), 0 for a length out of its limits; not kv->lens itself.  first, recent >= 0, first + recent <= keep, keep >= 1. */
 ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t ldw, const int32_t* dst_table,
                             int dst_pages, int keep, int first, int recent, int32_t* kept, float* weights_out,
                             int64_t ldw_out, int32_t* lens_out, void* stream);

@@ -37,7 +37,7 @@ def verify(target=P, ldt=100, draft=P, ldd=100, tokens=P, start=P, rows=6, batch
 
 INVALID, SHAPE, UNSUPPORTED = ms.MS_ERR_INVALID_ARG, ms.MS_ERR_SHAPE, ms.MS_ERR_UNSUPPORTED
 CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID), (dict(elem=3), INVALID),
-          (dict(elem=-1), INVALID), (dict(k=P + 8), INVALID), (dict(v=P + 2), INVALID), (dict(page_size=8), SHAPE), (dict(page_size=48), SHAPE),
+          (dict(elem=-1), INVALID), (dict(table=P + 2), INVALID), (dict(lens=P + 1), INVALID), (dict(status=P + 2), INVALID), (dict(k=P + 8), INVALID), (dict(v=P + 2), INVALID), (dict(page_size=8), SHAPE), (dict(page_size=48), SHAPE),
           (dict(page_size=0), SHAPE), (dict(page_size=-16), SHAPE), (dict(head_dim=80), SHAPE), (dict(n_kv_heads=0), SHAPE),
           (dict(n_kv_heads=5000), SHAPE), (dict(n_pages=0), SHAPE), (dict(batch=0), SHAPE), (dict(batch=1025), SHAPE), (dict(max_pages=0), SHAPE),
           (dict(max_pages=1 << 26), SHAPE), (dict(page_stride=2047), SHAPE), (dict(page_stride=2052), SHAPE), (dict(page_stride=-2048), SHAPE),
@@ -56,7 +56,7 @@ def test_no_cache_and_no_status_word():
     assert L.ms_op_rope_append_paged(None, P, 512, P, 128, P, 128, 1, 5, 8, P, None, P, 64, 0, 1.0, P, 512, None) == INVALID
     assert L.ms_op_attn_paged(None, P, 512, 1, 5, 4, 8, 0.125, P, P, 512, None, 0, P, 1 << 30, None) == INVALID
     assert L.ms_op_evict_paged(None, P, 64, P, 2, 32, 4, 8, P, P, 64, P, None) == INVALID
-    assert L.ms_op_status(None, None) == INVALID
+    assert L.ms_op_status(None, None) == INVALID and L.ms_op_status(P + 2, None) == INVALID
 
 
 @pytest.mark.parametrize("change,want", [
@@ -64,7 +64,7 @@ def test_no_cache_and_no_status_word():
     (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(elem=ms.MS_ELEM_BF16), UNSUPPORTED), (dict(elem=7), UNSUPPORTED),
     (dict(rot=-2), SHAPE), (dict(rot=63), SHAPE), (dict(rot=66), SHAPE), (dict(heads=0), SHAPE), (dict(heads=1 << 20), SHAPE), (dict(ldq=511), SHAPE),
     (dict(ldk=127), SHAPE), (dict(ldv=0), SHAPE), (dict(ldo=-512), SHAPE), (dict(ldk=1 << 50), SHAPE), (dict(k=P + 1), INVALID),
-    (dict(freq=P + 4), INVALID)])
+    (dict(freq=P + 4), INVALID), (dict(start=P + 2), INVALID), (dict(positions=P + 1), INVALID)])
 def test_rope_refuses(change, want):
     assert rope(**change) == want
 
@@ -78,7 +78,7 @@ def test_rope_of_no_rows_is_nothing():
     (dict(ws=P + 128), INVALID), (dict(elem=ms.MS_ELEM_BF16), UNSUPPORTED), (dict(most=0), SHAPE), (dict(most=65), SHAPE), (dict(heads=7), SHAPE),
     (dict(heads=0), SHAPE), (dict(heads=2 * 257, ldq=1 << 20, ldo=1 << 20), SHAPE), (dict(ldq=500), SHAPE), (dict(ldo=0), SHAPE),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(weights=P, ldw=63), SHAPE), (dict(weights=P + 2, ldw=64), INVALID),
-    (dict(q=P + 1), INVALID)])
+    (dict(q=P + 1), INVALID), (dict(start=P + 2), INVALID)])
 def test_attention_refuses(change, want):
     assert attn(**change) == want
     if set(change) <= {"most", "heads", "elem"}:
@@ -105,7 +105,8 @@ def test_attention_refuses_sizes_whose_tiles_do_not_fit_31_bits():
     (dict(weights=None), INVALID), (dict(dst=None), INVALID), (dict(kept=None), INVALID), (dict(out=None), INVALID), (dict(lens=None), INVALID),
     (dict(lens=P), INVALID), (dict(keep=0), SHAPE), (dict(first=-1), SHAPE), (dict(recent=-1), SHAPE), (dict(first=20, recent=13), SHAPE),
     (dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), SHAPE), (dict(pages=0), SHAPE), (dict(pages=1), SHAPE), (dict(ldw=63), SHAPE), (dict(ldo=31), SHAPE),
-    (dict(out=P, ldo=65), SHAPE)])
+    (dict(out=P, ldo=65), SHAPE), (dict(weights=P + 2), INVALID), (dict(dst=P + 1), INVALID), (dict(kept=P + 2), INVALID), (dict(out=P + 2), INVALID),
+    (dict(lens=P + 6), INVALID)])
 def test_eviction_refuses(change, want):
     assert evict(**change) == want
 
@@ -113,7 +114,9 @@ def test_eviction_refuses(change, want):
 @pytest.mark.parametrize("change,want", [
     (dict(target=None), INVALID), (dict(start=None), INVALID), (dict(us=None), INVALID), (dict(accepted=None), INVALID), (dict(out=None), INVALID),
     (dict(tokens=None), INVALID), (dict(ua=None), INVALID), (dict(rows=-1), SHAPE), (dict(batch=0), SHAPE), (dict(batch=(1 << 20) + 1), SHAPE),
-    (dict(vocab=0), SHAPE), (dict(most=-1), SHAPE), (dict(most=257), SHAPE), (dict(ldt=99), SHAPE), (dict(ldd=99), SHAPE), (dict(ldt=1 << 50), SHAPE)])
+    (dict(vocab=0), SHAPE), (dict(most=-1), SHAPE), (dict(most=257), SHAPE), (dict(ldt=99), SHAPE), (dict(ldd=99), SHAPE), (dict(ldt=1 << 50), SHAPE),
+    (dict(target=P + 2), INVALID), (dict(draft=P + 2), INVALID), (dict(tokens=P + 1), INVALID), (dict(start=P + 2), INVALID), (dict(ua=P + 2), INVALID),
+    (dict(us=P + 2), INVALID), (dict(accepted=P + 2), INVALID), (dict(out=P + 2), INVALID)])
 def test_verification_refuses(change, want):
     assert verify(**change) == want
 

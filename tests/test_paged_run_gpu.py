@@ -1,6 +1,10 @@
 """The paged-cache operators together, as a server runs them: append, attend, verify, cut back, go on; eagerly and in a
 captured graph.  Each step is held against the 64-bit restatements on what the cache then holds.  Tolerances are those
 of test_paged_gpu.py."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -347,3 +351,65 @@ def test_verify_refuses_random_numbers_outside_their_range():
             ms.op_status(status)
         assert e.value.status == ms.MS_ERR_TOKEN_RANGE
         assert out[0, 0].item() >= 0 and out[1, 0].item() == -1 and acc.cpu().tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("kq,kkv", R.PAIRS)
+@pytest.mark.parametrize("lens", [[1500, 64, 0, 700], [300, 64, 0, 70]])
+def test_attention_in_place_of_its_queries(kq, kkv, lens):
+    pages = R.Pages(lens, 2, 16, 64, kkv, seed=261)
+    counts = [2, 1, 1, 3]
+    q = torch.randn((7, 8, 64), generator=torch.Generator().manual_seed(12)).to(R.TYPES[kq])
+    x = q.cuda()
+    assert ms.attn_paged(pages.cuda(ms), x, R.starts(counts).cuda(), 3, out=x) is x
+    ref, A, spread, _ = R.attention(pages, q, counts, 0.125)
+    T = np.repeat(np.array(lens), counts)[:, None]
+    assert np.all(np.abs(R.f64(x) - ref) <= _attn_tol(kq, kkv, 64, T, ref, A, spread))
+
+
+def test_rope_turns_back_at_negative_positions():
+    pages = R.Pages([6], 2, 16, 64, "f32", seed=271)
+    x = torch.randn((6, 2, 64), generator=torch.Generator().manual_seed(4))
+    f = _freqs(64)
+    pos = np.array([-1, -17, -1000, -65537, 0, -(2 ** 20)])
+    out = ms.rope_append_paged(pages.cuda(ms), x.cuda(), x.cuda(), x.cuda(), R.starts([6]).cuda(), f.cuda(),
+                               positions=torch.tensor(pos, dtype=torch.int32).cuda())
+    want = R.rotate(R.f64(x), pos, f.numpy(), False, 1.0)
+    assert np.all(np.abs(R.f64(out) - want) <= _rope_tol("f32", want, R.f64(x), 1.0))
+
+
+FIRST = """
+import numpy as np, torch
+import paged_ref as R
+import decoder_only_transformer_int4_b200 as ms
+pages = R.Pages([1300, 40], 1, 16, 64, "f16", seed=5, spare=60)
+kv = pages.cuda(ms)
+q = torch.randn((2, 4, 64), generator=torch.Generator().manual_seed(1)).half()
+dq, st = q.cuda(), R.starts([1, 1]).cuda()
+w = torch.zeros((2, 1, kv.capacity), device="cuda")
+dst = torch.tensor(pages.free[:4], dtype=torch.int32).reshape(2, 2).cuda()
+p = torch.softmax(torch.randn((2, 50), generator=torch.Generator().manual_seed(2)), 1).cuda()
+none, u = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.rand(2, device="cuda")
+k, f, empty = torch.zeros((2, 1, 64), device="cuda").half(), torch.ones(32, dtype=torch.float64, device="cuda"), torch.zeros(0, device="cuda")
+ref, _, _, rw = R.attention(pages, q, [1, 1], 0.125)
+ZERO = R.starts([0, 0]).cuda()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):                     # nothing of the library has run yet
+    out = ms.attn_paged(kv, dq, st, 1, weights=w)
+    kept, new, lens = ms.evict_paged(kv, w, dst, 32)
+    acc, tok = ms.verify_draft(p, None, none, ZERO, 0, empty, u)
+    ms.rope_append_paged(kv, None, k, k, ZERO, f)
+graph.replay()
+torch.cuda.synchronize()
+assert np.abs(R.f64(out) - ref).max() < 2e-3, np.abs(R.f64(out) - ref).max()
+assert lens.cpu().tolist() == [32, 32] and acc.cpu().tolist() == [0, 0]
+assert np.abs(R.f64(w)[0, :, :1300] - rw[0]).max() < 1e-4
+print("done")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here]))
+    r = subprocess.run([sys.executable, "-c", FIRST], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
