@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a,
       const int j = j0 + u * per;
       src[u] = -1;
       if (j < n) {
-        const int i = __ldcg(kept + j);
-        const int sp = from_table[i >> a.c.page_shift], dp = to_table[j >> a.c.page_shift];
+        const int i = __ldcg(kept + j), to = j >> a.c.page_shift;
+        const int sp = from_table[i >> a.c.page_shift], dp = to < a.dst_pages ? to_table[to] : -1;
         if (sp < 0 || sp >= a.c.n_pages || dp < 0 || dp >= a.c.n_pages) {
           flag_error(a.c.status, kErrShape);
         } else {

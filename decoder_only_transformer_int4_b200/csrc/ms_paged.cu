@@ -210,9 +210,10 @@ ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t
   if (lens_out == kv->lens) return bad(MS_ERR_INVALID_ARG, who, "lens_out must not be the cache's lens");
   if (keep < 1 || first < 0 || recent < 0 || (int64_t)first + recent > keep)
     return bad(MS_ERR_SHAPE, who, "need keep >= 1, first, recent >= 0 and first + recent <= keep");
-  if (dst_pages < 1 || (int64_t)dst_pages * kv->page_size < keep) return bad(MS_ERR_SHAPE, who, "dst_table holds fewer than keep positions");
-  if (ldw < (int64_t)kv->max_pages * kv->page_size || ldw_out < keep || ldw > (1ll << 40) || ldw_out > (1ll << 40))
-    return bad(MS_ERR_SHAPE, who, "need ldw >= max_pages * page_size and ldw_out >= keep");
+  const int64_t capacity = (int64_t)kv->max_pages * kv->page_size;
+  if (dst_pages < 1) return bad(MS_ERR_SHAPE, who, "need dst_pages >= 1");
+  if (ldw < capacity || ldw_out < (keep < capacity ? keep : capacity) || ldw > (1ll << 40) || ldw_out > (1ll << 40))
+    return bad(MS_ERR_SHAPE, who, "need ldw >= max_pages * page_size and ldw_out >= min(keep, max_pages * page_size)");
   if (weights_out == weights && ldw_out != ldw) return bad(MS_ERR_SHAPE, who, "in place, ldw_out must be ldw");
   if (kv->n_kv_heads > 65535) return bad(MS_ERR_SHAPE, who, "too many heads");
   ms::EvictArgs a{view(*kv), weights, ldw, dst_table, dst_pages, keep, first, recent, kept, weights_out, ldw_out, lens_out};

@@ -435,12 +435,13 @@ ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, in
  * and the last `recent` positions are kept, and of the others those of largest weight until
  * keep are kept (ties: the lowest index; NaN counts as largest); a sequence of at most keep positions
  * keeps all.  The kept rows of K and V are copied in the order of their positions to positions
- * 0, 1, .. of the pages that dst_table (int32 [batch][dst_pages], dst_pages * page_size >= keep)
- * gives the sequence, of the same page arrays.  The pages of dst_table must not be read by
+ * 0, 1, .. of the pages that dst_table (int32 [batch][dst_pages]) gives the sequence, of the same page
+ * arrays; a row for which it has no page (dst_pages need only hold what the longest sequence keeps) is left out and flagged.  The pages of dst_table must not be read by
  * this call's sequences (kv->table), except that a sequence which keeps all may keep its pages: the same entries in both.
  * weights fp32 [batch][n_kv_heads][ldw] -> weights_out [batch][n_kv_heads][ldw_out], the kept positions'
  * weights in the new order and 0 behind; weights_out may be weights (with ldw_out = ldw), else
- * they must not overlap.  ldw >= max_pages * page_size, ldw_out >= keep.
+ * they must not overlap.  ldw >= max_pages * page_size, ldw_out >= min(keep, max_pages *
+ * page_size).
  * kept int32 [batch][n_kv_heads][keep]: the old positions, -1 behind.  lens_out int32 [batch]:
  * min(lens, keep), 0 for a length out of its limits; not kv->lens itself.  first, recent >= 0, first + recent <= keep, keep >= 1. */
 ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t ldw, const int32_t* dst_table,

@@ -104,7 +104,7 @@ def test_attention_refuses_sizes_whose_tiles_do_not_fit_31_bits():
 @pytest.mark.parametrize("change,want", [
     (dict(weights=None), INVALID), (dict(dst=None), INVALID), (dict(kept=None), INVALID), (dict(out=None), INVALID), (dict(lens=None), INVALID),
     (dict(lens=P), INVALID), (dict(keep=0), SHAPE), (dict(first=-1), SHAPE), (dict(recent=-1), SHAPE), (dict(first=20, recent=13), SHAPE),
-    (dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), SHAPE), (dict(pages=0), SHAPE), (dict(pages=1), SHAPE), (dict(ldw=63), SHAPE), (dict(ldo=31), SHAPE),
+    (dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), SHAPE), (dict(pages=0), SHAPE), (dict(ldw=63), SHAPE), (dict(ldo=31), SHAPE), (dict(keep=100, ldo=63), SHAPE),
     (dict(out=P, ldo=65), SHAPE), (dict(weights=P + 2), INVALID), (dict(dst=P + 1), INVALID), (dict(kept=P + 2), INVALID), (dict(out=P + 2), INVALID),
     (dict(lens=P + 6), INVALID)])
 def test_eviction_refuses(change, want):

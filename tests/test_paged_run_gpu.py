@@ -268,6 +268,35 @@ def test_evict_over_a_cluster(T, keep, first, recent, in_place):
     assert torch.equal(k[src], k0[src]) and torch.equal(v[src], v0[src])
 
 
+def test_evict_keeps_more_than_the_tables_hold():
+    # no sequence reaches keep: narrower tables and weights than keep are enough
+    lens, hk, page, keep = [50, 3, 0, 33], 2, 16, 200
+    pages = R.Pages(lens, hk, page, 64, "bf16", seed=281, spare=20)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = pages.cuda(ms, status)
+    w = torch.rand((4, hk, kv.capacity), device="cuda")
+    assert kv.capacity < keep
+    dst = torch.full((4, 4), 1 << 29, dtype=torch.int32)
+    for b, t in enumerate(lens):
+        for j in range(-(-t // page)):
+            dst[b, j] = pages.free.pop()
+    for narrow in (4, 3):
+        kept, new, nl = ms.evict_paged(kv, w, dst[:, :narrow].contiguous().cuda(), keep, first=3, recent=100)
+        if narrow == 4:
+            ms.op_status(status)
+        else:                                  # the first sequence's last two rows have no page: left out and flagged
+            with pytest.raises(ms.MsError):
+                ms.op_status(status)
+        assert nl.cpu().tolist() == lens
+        k = R.f64(pages.dk)
+        for b, t in enumerate(lens):
+            src = pages.rows("k", b)
+            assert np.array_equal(kept[b, 0].cpu().numpy(), list(range(t)) + [-1] * (keep - t))
+            assert torch.equal(new[b, :, :t], w[b, :, :t]) and not new[b, :, t:].any()
+            for j in range(min(t, narrow * page)):
+                assert np.array_equal(k[int(dst[b, j // page]), :, j % page], src[:, j])
+
+
 # ---- the handle, other streams -------------------------------------------------------------------------
 
 def test_the_cache_keeps_its_tensors_and_is_read_only():
