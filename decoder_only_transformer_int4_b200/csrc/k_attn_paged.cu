@@ -89,7 +89,9 @@ struct Shape {
   static constexpr int R = 8 * NB;
   static constexpr int kRowBytes = HD * sizeof(KT);
   static constexpr int kStageBytes = 2 * kStep * kRowBytes;      // K then V of one warp's step
-  static constexpr int kStages = kStageBytes <= 4096 ? 3 : 2;
+  // 16 KB (fp32, 128 elements): one stage and three CTAs an SM instead of two stages and one CTA
+  // (67 sequences of 20 heads on 5: 37 us, 48 with two stages)
+  static constexpr int kStages = kStageBytes <= 4096 ? 3 : kStageBytes <= 8192 ? 2 : 1;
   static constexpr int kQBytes = R * HD * ((kF32 || Q32) ? 4 : 2);   // Q32 on halves: hi and lo planes
   static constexpr bool kQRegs = !kF32 && NB * (HD / 16) * (Q32 ? 2 : 1) <= 16;   // Q's fragments stay in registers
   static constexpr int kObufStride = HD + 4;
@@ -428,9 +430,11 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
 
   for (int it = 0; it < niter; ++it) {
     {
+      // the next copies' tiles, and the one behind this for its unit's rows
+      constexpr int kAhead = kStages > 1 ? kStages - 1 : 1;
+      if (it + kAhead < niter && ((it + kAhead) & (kRing / 2 - 1)) == 0) look_up(it + kAhead);
       const int nx = it + kStages - 1;
       if (nx < niter) {
-        if ((nx & (kRing / 2 - 1)) == 0) look_up(nx);
         issue(nx);
       } else {
         cp_commit();
@@ -963,7 +967,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
 // ---------------------------------------------------------------------------------
 constexpr int kFinishThreads = 256, kFinishWarps = kFinishThreads / 32, kStatRows = 64;
 constexpr int kWeightTile = 1024;   // positions of a weighing CTA
-constexpr int kLeastSlice = 16;   // elements of a head that a joining CTA writes, at least
+constexpr int kLeastItems = 16;   // of four elements each that a joining CTA writes, at least
 
 // The pieces of a cut unit: piece k is the second slot of CTA c0 (it begins the unit), or the first slot of CTA c0 + k.
 struct Cut {
@@ -1095,11 +1099,14 @@ __global__ void __launch_bounds__(kFinishThreads) attn_finish_kernel(Kargs a, in
       if (t[p] < T) to[t[p]] = was[p] + w[p];
     return;
   }
-  const int unit = blockIdx.x / slices, slice = hd / slices, e0 = (blockIdx.x - unit * slices) * slice;
+  const int unit = blockIdx.x / slices;
   const int kvh = unit / a.rb, rt = unit - kvh * a.rb;
   const int row0 = rt * R, real = min(R, rows - row0);
   if (real <= 0) return leave();
-  const int vecs = slice / 4, items = real * vecs;   // four elements of a row each
+  // this CTA's share of the unit's rows, in items of four elements
+  const int vecs = hd / 4, share = (real * vecs + slices - 1) / slices, base = (blockIdx.x - unit * slices) * share;
+  const int items = min(share, real * vecs - base);
+  if (items <= 0) return leave();
   auto out = [&](int r, int e) {
     const int rr = row0 + r, row = rr / a.hpg, h = rr - row * a.hpg;
     return static_cast<QT*>(a.out) + (r0 + row) * a.ldo + (long long)(kvh * a.hpg + h) * hd + e;
@@ -1108,7 +1115,7 @@ __global__ void __launch_bounds__(kFinishThreads) attn_finish_kernel(Kargs a, in
     pdl_wait();   // rows may be read before the main kernel by none of ours, but order their writes all the same
     pdl_trigger();
     for (int i = tid; i < items; i += kFinishThreads)
-      for (int k = 0; k < 4; ++k) out(i / vecs, e0 + 4 * (i % vecs))[k] = rounded<QT>(0.f);
+      for (int k = 0; k < 4; ++k) out((base + i) / vecs, 4 * ((base + i) % vecs))[k] = rounded<QT>(0.f);
     return;
   }
   const Cut cut = find_cut(a, first, total, kvh, rt, rts, per);
@@ -1116,7 +1123,7 @@ __global__ void __launch_bounds__(kFinishThreads) attn_finish_kernel(Kargs a, in
   if (pieces == 1) return leave();
   // threads that share an item's pieces, or items a thread
   const int parts = max(1, min(pieces, kFinishThreads / items)), part = parts > 1 ? tid / items : 0;
-  int item = parts > 1 ? tid - part * items : tid, r = item / vecs, e = e0 + 4 * (item - r * vecs);
+  int item = parts > 1 ? tid - part * items : tid, r = (base + item) / vecs, e = 4 * (base + item - r * vecs);
   constexpr int U = 4;
   pdl_wait();
   pdl_trigger();
@@ -1132,7 +1139,7 @@ __global__ void __launch_bounds__(kFinishThreads) attn_finish_kernel(Kargs a, in
     }
   };
   load(part);
-  for (int q = warp; q < real; q += kFinishWarps) {
+  for (int q = base / vecs + warp; q <= (base + items - 1) / vecs; q += kFinishWarps) {
     const float2 ml = cut_row(a, cut, R, q, lane);
     if (lane == 0) {
       sM[q] = ml.x == -INFINITY ? 0.f : ml.x;
@@ -1178,8 +1185,8 @@ __global__ void __launch_bounds__(kFinishThreads) attn_finish_kernel(Kargs a, in
     }
     item += kFinishThreads;
     if (parts > 1 || item >= items) return;
-    r = item / vecs;
-    e = e0 + 4 * (item - r * vecs);
+    r = (base + item) / vecs;
+    e = 4 * (base + item - r * vecs);
     load(0);
   }
 }
@@ -1268,7 +1275,7 @@ cudaError_t attn_go(const Launch& L, const AttnPagedArgs& a, int n_sm, void* ws)
   });
   // few units: several CTAs join each, so that every load of theirs is under way at once
   k.slices = 1;
-  while (k.slices < HD / kLeastSlice && (long long)a.c.batch * a.c.Hk * p.rb * k.slices < n_sm) k.slices *= 2;
+  while (k.slices * kLeastItems < p.R * HD / 4 && (long long)a.c.batch * a.c.Hk * p.rb * k.slices < n_sm) k.slices *= 2;
   const int joins = p.cluster ? 0 : a.c.Hk * p.rb * k.slices;
   const int adds = a.weights ? a.c.Hk * ((a.c.capacity() + kWeightTile - 1) / kWeightTile) : 0;
   if (e != cudaSuccess || joins + adds == 0) return e;

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
+#include <algorithm>
 #include "ms_device.cuh"
 #include "ms_launch.cuh"
 #include "ms_paged.h"
@@ -78,7 +79,7 @@ __device__ __forceinline__ void pack(Pack<__nv_bfloat16, N>& p, const float (&y)
 // 4132 rows of 48 bf16 heads of 128: 25 us, 4.0 TB/s (the chain and the last wave show); 64 rows: 3.2 us.
 // ---------------------------------------------------------------------------------
 namespace {
-constexpr int kRopeThreads = 256, kRopeTokens = 8, kRopeItems = 2;
+constexpr int kRopeThreads = 256, kRopeTokens = 32, kRopeItems = 2;
 
 struct TokInfo {
   long long dst;   // element offset of kv head 0's row in the pages, -1: not appended
@@ -93,29 +94,25 @@ struct alignas(16) Sines {
 
 // Sequence, place and sines of the block's tokens; for all its threads, a barrier at the end.
 __device__ __forceinline__ void rope_tokens(const RopeArgs& a, int t0, int nt, Sines (&cs)[kRopeTokens], TokInfo (&info)[kRopeTokens]) {
-  __shared__ int seq[kRopeTokens];
+  __shared__ int marks[kRopeTokens];
   const int tid = threadIdx.x, half = a.rot >> 1;
-  if (tid < kRopeTokens) seq[tid] = 0;
-  __syncthreads();
-  // the sequence of token t: how many row_start[i + 1] are <= t
-  int mine[kRopeTokens];
-#pragma unroll
-  for (int k = 0; k < kRopeTokens; ++k) mine[k] = 0;
-  for (int i = tid; i < a.c.batch; i += kRopeThreads) {
-    const int end = a.row_start[i + 1];
-#pragma unroll
-    for (int k = 0; k < kRopeTokens; ++k) mine[k] += end <= t0 + k;
-  }
-#pragma unroll
-  for (int k = 0; k < kRopeTokens; ++k)
-    if (k < nt) {
-      const int all = __reduce_add_sync(0xffffffffu, mine[k]);
-      if ((tid & 31) == 0 && all) atomicAdd(&seq[k], all);
+  // The sequence of token t: how many row_start[i + 1] are <= t.  Those <= t0 are counted, the others among the
+  // block's tokens marked where they end.
+  if (tid < kRopeTokens) marks[tid] = 0;
+  int before = 0;
+  for (int i0 = 0; i0 < a.c.batch; i0 += kRopeThreads) before += __syncthreads_count(i0 + tid < a.c.batch && a.row_start[i0 + tid + 1] <= t0);
+  if (nt > 1) {
+    for (int i = tid; i < a.c.batch; i += kRopeThreads) {
+      const int end = a.row_start[i + 1];
+      if (end > t0 && end < t0 + nt) atomicAdd(&marks[end - t0], 1);
     }
-  __syncthreads();
+    __syncthreads();
+  }
   for (int it = tid; it < nt * max(half, 1); it += kRopeThreads) {
     const int k = it / max(half, 1), j = it - k * max(half, 1);
-    const int t = t0 + k, b = seq[k];
+    int b = before;
+    for (int i = 1; i <= k; ++i) b += marks[i];
+    const int t = t0 + k;
     const bool live = b < a.c.batch;   // rows behind the last sequence are left as they were
     int place = 0, r0 = 0, r1 = 0;
     if (live) {
@@ -302,10 +299,12 @@ static cudaError_t rope_go(const Launch& L, const RopeArgs& a) {
   // 16-byte accesses need aligned rows, and half-layout pairs that fall on whole chunks
   const bool vector = !off(a.q, a.ldq) && !off(a.k, a.ldk) && !off(a.v, a.ldv) && !off(a.q ? a.q_out : nullptr, a.ldo) &&
                       (a.interleaved || a.rot % (2 * VEC) == 0);
-  // Tokens a block, a power of two: more of them share the chain, but 1.5 waves of blocks have to be left to
-  // overlap one block's chain with another's copies (4132 rows: 26.7 us at 8, 25.2 at 4; 32767: 98 at 8, 103 at 4)
-  int tokens = 1;
-  while (tokens < kRopeTokens && a.rows >= 148 * 6 * 2 * tokens) tokens *= 2;
+  // Tokens a block, a power of two: more of them share the chain.  Two for each thread to move at least, where that leaves
+  // two blocks an SM (27600 rows of 3 heads: 13.7 us at 32 tokens, 26.3 at 8); up to 8 while 1.5 waves of blocks are
+  // left to overlap one block's chain with another's copies (4132 rows of 48 heads: 26.7 us at 8, 25.2 at 4; 32767 of 40: 98 at
+  // 8, 103 at 4, 105 at 16).
+  const int items = ((a.q ? a.H : 0) + 2 * a.c.Hk) * a.c.hd / (vector ? 2 * VEC : 2), most = std::min(kRopeTokens, kRopeThreads * 2 * VEC / a.c.hd);
+  while (tokens < most && a.rows >= 148 * 2 * 2 * tokens && (tokens * items < 2 * kRopeThreads || (tokens < 8 && a.rows >= 148 * 6 * 2 * tokens))) tokens *= 2;
   const dim3 grid((a.rows + tokens - 1) / tokens), block(kRopeThreads);
   if (vector) return launch_k(L, rope_append_paged_kernel<QT, KT, true>, grid, block, 0, a, tokens);
   return launch_k(L, rope_append_paged_kernel<QT, KT, false>, grid, block, 0, a, tokens);
@@ -568,9 +567,12 @@ cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a) {
   const int chunks = a.c.hd * (a.c.elem == kF32 ? 4 : 2) / 16;   // 8, 16 or 32
   const int shift = chunks == 8 ? 3 : chunks == 16 ? 4 : 5;
   const long long units = (long long)a.c.Hk * a.c.batch;
-  // more CTAs a unit while two a SM are not reached and each warp has 64 positions
+  // More CTAs a unit, up to two an SM, while each has 64 positions a warp or 128 KB of rows.  Few units want many CTAs for
+  // their rows (12 units of 1310 fp32 rows of 128: 17 us in clusters of 8, 34 in pairs), small ones are faster without the
+  // cluster's barriers (52 units of 170 rows of 256 bytes: 9.6 us alone, 13.8 in fours).
+  const long long bytes = (long long)std::min(a.keep, a.c.capacity()) * chunks * 16 * 2;
   int C = 1;
-  while (C < kEvMaxCluster && units * C < 2 * 148 && a.c.capacity() > C * 2 * kEvThreads) C *= 2;
+  while (C < kEvMaxCluster && units * C * 2 <= 2 * 148 && (bytes > C * (128ll << 10) || a.c.capacity() > C * 2 * kEvThreads)) C *= 2;
   return launch_cluster(L, evict_paged_kernel, C, dim3((unsigned)(units * C)), dim3(kEvThreads), 0, a, shift);
 }
 

@@ -442,3 +442,32 @@ def test_the_first_calls_of_a_process_may_be_captured():
     env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here]))
     r = subprocess.run([sys.executable, "-c", FIRST], env=env, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("kq,kkv", R.PAIRS)
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_runs_of_many_tiles_over_several_units(kq, kkv, hd):
+    # every CTA goes through more than 16 tiles (its descriptors are looked up in parts) and from unit to unit on the way
+    g = torch.Generator(device="cuda").manual_seed(291)
+    lens = [7000 + (977 * i) % 1300 for i in range(80)]
+    group, page, scale = 2, 64, hd ** -0.5
+    need = [-(-t // page) for t in lens]
+    order = torch.randperm(sum(need), generator=g, device="cuda").to(torch.int32)
+    table = torch.zeros((80, max(need)), dtype=torch.int32, device="cuda")
+    for b, (n, o) in enumerate(zip(need, np.cumsum([0] + need))):
+        table[b, :n] = order[o:o + n]
+    k = torch.randn((sum(need), 1, page, hd), generator=g, device="cuda").to(R.TYPES[kkv])
+    v = torch.randn((sum(need), 1, page, hd), generator=g, device="cuda").to(R.TYPES[kkv])
+    q = torch.randn((80, group, hd), generator=g, device="cuda").to(R.TYPES[kq])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = ms.PagedKV(k, v, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), status)
+    out = R.f64(ms.attn_paged(kv, q, R.starts([1] * 80).cuda(), 1))
+    ms.op_status(status)
+    for b, t in enumerate(lens):
+        kb = k[table[b, :need[b]].long(), 0].reshape(-1, hd)[:t].double()
+        vb = v[table[b, :need[b]].long(), 0].reshape(-1, hd)[:t].double()
+        p = torch.softmax((q[b].double() @ kb.T) * scale, 1)
+        spread = (scale * (q[b].double().abs() @ kb.abs().T)).amax(1)
+        ref, A = R.f64(p @ vb), R.f64(p @ vb.abs())
+        tol = _attn_tol(kq, kkv, hd, np.full(group, t), ref, A, R.f64(spread))
+        assert np.all(np.abs(out[b] - ref) <= tol), b
