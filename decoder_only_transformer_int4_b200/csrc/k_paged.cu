@@ -303,6 +303,7 @@ static cudaError_t rope_go(const Launch& L, const RopeArgs& a) {
   // two blocks an SM (27600 rows of 3 heads: 13.7 us at 32 tokens, 26.3 at 8); up to 8 while 1.5 waves of blocks are
   // left to overlap one block's chain with another's copies (4132 rows of 48 heads: 26.7 us at 8, 25.2 at 4; 32767 of 40: 98 at
   // 8, 103 at 4, 105 at 16).
+  int tokens = 1;
   const int items = ((a.q ? a.H : 0) + 2 * a.c.Hk) * a.c.hd / (vector ? 2 * VEC : 2), most = std::min(kRopeTokens, kRopeThreads * 2 * VEC / a.c.hd);
   while (tokens < most && a.rows >= 148 * 2 * 2 * tokens && (tokens * items < 2 * kRopeThreads || (tokens < 8 && a.rows >= 148 * 6 * 2 * tokens))) tokens *= 2;
   const dim3 grid((a.rows + tokens - 1) / tokens), block(kRopeThreads);
