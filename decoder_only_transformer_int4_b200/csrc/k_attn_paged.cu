@@ -6,21 +6,32 @@
 // heads of group g.
 //
 // Bound: HBM, every K and V row of a sequence is read once for all heads of its group and all newest
-// rows (2 T Hk hd elements).  The arithmetic stays on warp-level MMAs: the rows of a (sequence, kv head)
-// - at most 16 or 32 at a time - are the M side, sixteen cached positions a step the N side.  A group
-// of 1 to 32 rows fills no 128-row tile, so a wider tensor instruction would spend its time on padding
-// while the memory waits all the same.
+// rows, up to 32 at a time (2 T Hk hd elements).  One cache of 131071 positions (8 kv heads of 64, fp16) takes 48 us with
+// the join, 5.5 TB/s; 16 ragged sequences of up to 16411 (8 heads of 128, bf16) 98 us at one row each (6.1 TB/s)
+// and 115 us at up to six, where a tile of 24 rows costs about as many issue slots as the memory leaves.  64 sequences
+// of 505 to 1024 take 17.5 us (19.4 with weights) for 52 MB: 4.5 us until the first tile is there, then seven tiles
+// a CTA, then the join.
+//
+// The products stay on warp-level MMAs: S^T = K Q^T and O^T = V^T P^T, sixteen cached positions (or elements
+// of a head) on the M side, rows in tiles of 8 on the N side, so that the 3 or 4 rows of a decoding group pad to 8.
+// tcgen05 was built and measured for more than 16 rows (128 positions a tile, one to a TMEM lane): 200 us against 115 on
+// the case above, 100 against 83 at 56 rows.  Its products are short; what a tile costs is its copies through the
+// load-store path and the softmax of its rows, which eight warps there do in step and twelve here do each in its own time.
 //
 // Split.  The positions of all (sequence, kv head, row tile) units are cut into tiles of 64 and laid
 // end to end; every resident CTA takes an equal run of tiles, whatever the lengths.  A run crosses
 // units: a unit that lies in one CTA is finished there, a cut one leaves (m, l, o) partials, one slot
 // for the piece that begins a CTA's run and one for the piece that ends it, which attn_finish_kernel adds.
 // Nothing waits for another CTA, no counter has to be cleared, and the order of every sum is fixed.
+// A call whose units all fit the GPU as clusters with at most two tiles to a CTA (1024 positions) joins over
+// distributed shared memory instead, in one launch: one fp32 stream of 577 positions 6.9 us, 9.5 in two kernels; with eight
+// tiles to a CTA (4000 positions) the cluster's 14.1 us lose to 8.8.
 //
 // Inside a CTA each warp takes its own 16 positions of every tile and streams them with cp.async
 // through its own ring, so the warps meet only at a unit's end.  16 positions lie within one page (a
 // page holds a power of two of at least 16 positions), so a step needs one table entry; the entries of
-// the next 32 tiles are looked up at once, one per lane.
+// the next 16 tiles are looked up at once, one per lane.  Two to three CTAs share an SM: with one, four warps
+// cannot hide a step's chain of loads, products and exponentials (drafted rows: 211 us).
 //
 // Arithmetic.  16-bit caches: products of m16n8k16 with fp32 sums; the probabilities enter P V as a
 // 16-bit pair hi + lo (two MMAs), so that they carry 16 (bf16) or 22 (fp16) bits and not 8 or 11: the

@@ -471,3 +471,49 @@ def test_attention_runs_of_many_tiles_over_several_units(kq, kkv, hd):
         ref, A = R.f64(p @ vb), R.f64(p @ vb.abs())
         tol = _attn_tol(kq, kkv, hd, np.full(group, t), ref, A, R.f64(spread))
         assert np.all(np.abs(out[b] - ref) <= tol), b
+
+
+def test_offsets_past_32_bits():
+    # four pages 2^31 elements and more apart, in one allocation of 13 GB; rows of probabilities as far apart
+    hk, page, hd, T = 2, 64, 64, 150
+    size, stride = hk * page * hd, 2 ** 31 + 64
+    flat = torch.empty(3 * stride + 2 * size, dtype=torch.float16, device="cuda")
+    k = flat.as_strided((4, hk, page, hd), (stride, page * hd, hd, 1), 0)
+    v = flat.as_strided((4, hk, page, hd), (stride, page * hd, hd, 1), size)
+    for x in (k, v):
+        for i in range(4):
+            x[i].fill_(float("nan"))
+    pages = R.Pages([T], hk, page, hd, "f16", seed=301)
+    pages.table = torch.tensor([[3, 0, 2]], dtype=torch.int32)
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = ms.PagedKV(k, v, pages.table.cuda(), lens, status)
+    g = torch.Generator().manual_seed(302)
+    x, f = torch.randn((T, 4 + 2 * hk, hd), generator=g).half(), _freqs(hd)
+    d = x.cuda()
+    q = ms.rope_append_paged(kv, d[:, :4], d[:, 4:4 + hk], d[:, 4 + hk:], R.starts([T]).cuda(), f.cuda())
+    want = R.rotate(R.f64(x[:, :4 + hk]), np.arange(T), f.numpy(), False, 1.0)
+    for i in range(T):
+        got = R.f64(k[int(pages.table[0, i // page]), :, i % page])
+        assert np.all(np.abs(got - want[i, 4:]) <= _rope_tol("f16", want[i, 4:], R.f64(x[i, 4:4 + hk]), 1.0))
+    pages.k, pages.v, pages.lens = k.cpu(), v.cpu(), [T]
+    w = torch.zeros((1, hk, kv.capacity), device="cuda")
+    out = ms.attn_paged(kv, q[-2:].contiguous(), R.starts([2]).cuda(), 2, weights=w)
+    ref, A, spread, _ = R.attention(pages, q[-2:], [2], hd ** -0.5)
+    assert np.all(np.abs(R.f64(out) - ref) <= _attn_tol("f16", "f16", hd, np.array([[T]]), ref, A, spread))
+    kept, _, _ = ms.evict_paged(kv, w, torch.tensor([[1]], dtype=torch.int32, device="cuda"), 50, first=2, recent=20)
+    ms.op_status(status)
+    rows = [pages.rows("k", 0), pages.rows("v", 0)]
+    for h in range(hk):
+        ids = kept[0, h].cpu().numpy()
+        assert np.array_equal(R.f64(k[1, h, :50]), rows[0][h, ids]) and np.array_equal(R.f64(v[1, h, :50]), rows[1][h, ids])
+    V = 5000
+    target = flat.view(torch.float32)[:2 ** 31 + 8 + V].as_strided((2, V), (2 ** 31 + 8, 1), 0)
+    p = _probs(2, V, seed=303)
+    target.copy_(p)
+    u = torch.tensor([0.3], device="cuda")
+    tok = torch.tensor([int(p[0].argmax())], dtype=torch.int32)
+    for ua in (0.0, 1 - 2.0 ** -24):
+        acc, said = ms.verify_draft(target, None, tok.cuda(), R.starts([1]).cuda(), 1, torch.tensor([ua], device="cuda"), u)
+        taken, words = R.verify(p.numpy(), None, tok.numpy(), [1], np.array([ua]), u.cpu().numpy())
+        assert acc.cpu().tolist() == taken and said.cpu().tolist()[0] == words[0] + [-1] * (2 - len(words[0]))
