@@ -326,11 +326,12 @@ cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_e
 // lowest index; a NaN counts as largest).
 //
 // A cluster of CTAs shares a (sequence, kv head).  Each warp takes a contiguous run of the weights and
-// holds them in shared memory (up to 20 a lane; what is longer is read again from L2 in each pass).  A radix select over
-// the weights' ordered 32-bit keys (four 8-bit digits, the histograms added over distributed shared
-// memory; equal digits of a warp are counted together, so that the few distinct leading digits of
-// like-sized weights do not serialise on one counter) gives the key of the last one kept and how many of
-// its equals stay.  Then the kept positions get their ranks, in order, from the warps' counts, and the
+// holds their keys in shared memory (up to 16 a lane; what is longer is read again from L2 in each pass).  A radix select over
+// the weights' ordered 32-bit keys (8-bit digits, the histograms added over distributed shared
+// memory; equal leading digits of a warp are counted together, so that the few distinct ones of
+// like-sized weights do not serialise on one counter) narrows down the key of the last one kept; as soon as at most
+// 128 keys are left for it, every CTA gets them all and ranks them by comparing each with each.  That gives the key and how
+// many of its equals stay.  Then the kept positions get their ranks, in order, from the warps' counts, and the
 // cluster moves the kept weights and the rows of K and V, 16 bytes a thread, by rank: equal shares
 // for the CTAs wherever the kept ones lie.
 //
@@ -338,13 +339,15 @@ cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_e
 // never exceeds its position, so that a block's writes fall on positions that no later block reads.
 //
 // Bound: HBM, 2 x kept rows read and written (10.7 and 20.8 us at 64 x 4 x 512 rows of 128 bytes and
-// 4 x 8 x 4099 of 256); the select is latency, ~1 us a digit.  One CTA per (sequence, kv head) with a second
-// kernel for the rows took 26.9 and 78.4 us, of that the select 14 and 56; this takes 20.2 and 42.0 us (rows
-// 9 and 20, a digit 0.6 and, with the cluster's barrier and the sum of its histograms, 2).
+// 4 x 8 x 4099 of 256); the select is latency: a digit takes 0.6 us in one CTA, 2 to 2.4 in a cluster (its barrier 0.9, the sum of
+// its histograms 0.5).  20.2 and 38.8 us; all four digits 20.5 and 41.2; one CTA per (sequence, kv head) with a second
+// kernel for the rows 26.9 and 78.4, of that the select 14 and 56.  Moving the rows that stay in any case while the barriers are
+// waited for did not pay (21.8 and 44.5): their loads delay the select's.
 // ---------------------------------------------------------------------------------
 namespace {
 constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32, kEvMaxCluster = 8;
-constexpr int kEvHeld = 20;   // weights a thread holds in shared memory
+constexpr int kEvHeld = 16;   // weights a thread holds in shared memory
+constexpr int kEvFew = 128;   // so few candidates for the last place are ranked by comparing all with all
 constexpr int kEvRuns = kEvWarps * kEvMaxCluster;
 
 // Keys in the weights' order, all of them between those of a place without a position and of one that stays
@@ -354,13 +357,65 @@ __device__ __forceinline__ unsigned weight_key(float w) {
   const unsigned u = w != w ? 0x7f800001u : __float_as_uint(w + 0.0f);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
+
+// Rows of K and V of one (sequence, kv head) by rank: this block's share of the n of them, `blocks` blocks of kEvThreads in all.
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int row_shift, int b, int g, int n, int block, int blocks) {
+  const int tid = threadIdx.x;
+  const int* kept = a.kept + ((long long)b * a.c.Hk + g) * a.keep;
+  const int per = kEvThreads >> row_shift;            // rows a pass (1 << row_shift chunks of 16 bytes each)
+  const int c = tid & ((1 << row_shift) - 1);
+  const int mask = a.c.page() - 1;
+  const uint4* ks = static_cast<const uint4*>(a.c.k);
+  const uint4* vs = static_cast<const uint4*>(a.c.v);
+  uint4* kd = static_cast<uint4*>(a.c.k);
+  uint4* vd = static_cast<uint4*>(a.c.v);
+  const long long page16 = a.c.page_stride * (a.c.elem == kF32 ? 4 : 2) / 16;
+  const int* from_table = a.c.table + (long long)b * a.c.max_pages;
+  const int* to_table = a.dst_table + (long long)b * a.dst_pages;
+  constexpr int U = 4;
+  for (int j0 = block * per * U + (tid >> row_shift); j0 < n; j0 += blocks * per * U) {
+    long long src[U], dst[U];
+    uint4 xk[U], xv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * per;
+      src[u] = -1;
+      if (j < n) {
+        const int i = __ldcg(kept + j), to = j >> a.c.page_shift;
+        const int sp = from_table[i >> a.c.page_shift], dp = to < a.dst_pages ? to_table[to] : -1;
+        if (sp < 0 || sp >= a.c.n_pages || dp < 0 || dp >= a.c.n_pages) {
+          flag_error(a.c.status, kErrShape);
+        } else {
+          src[u] = sp * page16 + (((long long)g << a.c.page_shift) + (i & mask) << row_shift) + c;
+          dst[u] = dp * page16 + (((long long)g << a.c.page_shift) + (j & mask) << row_shift) + c;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (src[u] >= 0) {
+        xk[u] = ks[src[u]];
+        xv[u] = vs[src[u]];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (src[u] >= 0) {
+        kd[dst[u]] = xk[u];
+        vd[dst[u]] = xv[u];
+      }
+  }
+}
+
 }  // namespace
 
-__global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a, int row_shift) {
+__global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a, int row_shift, int rows_here) {
   namespace cg = cooperative_groups;
   __shared__ __align__(16) unsigned hist[4][256];
   __shared__ __align__(16) unsigned total[256];
-  __shared__ int picked[4][2];        // of each pass: the digit, how many of its keys are still wanted
+  __shared__ int picked[4][3];        // of each pass: the digit, how many of its keys are still wanted, how many there are
+  __shared__ __align__(16) unsigned few[kEvFew];
+  __shared__ unsigned last_key;
+  __shared__ int last_equal, few_count;   // few_count: the first CTA's counts for all
   __shared__ unsigned held[kEvHeld][kEvThreads];
   __shared__ int count[2][kEvRuns];   // of every warp of the cluster: kept for sure, equal to the last key
   cg::cluster_group cluster = cg::this_cluster();
@@ -369,6 +424,8 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   cluster.barrier_arrive();   // all CTAs have begun before one writes into another
   for (int i = tid; i < 4 * 256; i += kEvThreads) (&hist[0][0])[i] = 0;
+  if (tid < kEvFew) few[tid] = kKeyNone;
+  if (tid == 0) few_count = 0;
   pdl_wait();
   pdl_trigger();
   const float* w = a.weights + (long long)unit * a.ldw;
@@ -389,7 +446,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a,
   const int runs = C * kEvWarps, run = rank * kEvWarps + warp;
   const int kn = (T + 32 * runs - 1) / (32 * runs);
   const int i0 = run * kn * 32 + lane;   // below 2 (T + 32 runs) < 2^31
-  constexpr int kAtOnce = 10;
+  constexpr int kAtOnce = 8;
   static_assert(kEvHeld % kAtOnce == 0, "");
   for (int k0 = 0; k0 < min(kn, kEvHeld); k0 += kAtOnce) {
     float x[kAtOnce];
@@ -461,6 +518,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a,
           if (before < left && left <= before + c[k]) {   // T > keep: one bin has it
             picked[pass][0] = 8 * lane + 7 - k;
             picked[pass][1] = left - before;
+            picked[pass][2] = c[k];
           }
           before += c[k];
         }
@@ -468,9 +526,39 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a,
       __syncthreads();
       prefix = (prefix << 8) | (unsigned)picked[pass][0];
       left = picked[pass][1];
+      const int shifted = shift;
+      if (pass == 3) {
+        key = prefix;
+        equal = left;
+      } else if (picked[pass][2] <= kEvFew) {
+        // every CTA gets them all, in any order
+        each([&](int, unsigned u) {
+          if ((u >> shifted) == prefix) {
+            const int at = atomicAdd(cluster.map_shared_rank(&few_count, 0), 1);
+            for (int r = 0; r < C; ++r) cluster.map_shared_rank(few, r)[at] = u;
+          }
+        });
+        sync_all();
+        if (tid < picked[pass][2]) {
+          const unsigned u = few[tid];
+          int above = 0, same = 0;
+#pragma unroll 4
+          for (int j = 0; j < picked[pass][2]; j += 4) {   // behind the last one: kKeyNone, below all
+            const uint4 x = *reinterpret_cast<const uint4*>(few + j);
+            above += (x.x > u) + (x.y > u) + (x.z > u) + (x.w > u);
+            same += (x.x == u) + (x.y == u) + (x.z == u) + (x.w == u);
+          }
+          if (above < left && left <= above + same) {   // the same for all equal ones
+            last_key = u;
+            last_equal = left - above;
+          }
+        }
+        __syncthreads();
+        key = last_key;
+        equal = last_equal;
+        break;
+      }
     }
-    key = prefix;
-    equal = left;
   }
 
   // ranks in the order of the positions
@@ -519,49 +607,13 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a,
   for (long long j = n + rank * kEvThreads + tid; j < a.ldwo; j += C * kEvThreads) wo[j] = 0.f;
   if (g == 0 && rank == 0 && tid == 0) a.lens_out[b] = n;
 
-  // rows
-  const int per = kEvThreads >> row_shift;            // rows a pass (1 << row_shift chunks of 16 bytes each)
-  const int c = tid & ((1 << row_shift) - 1);
-  const int mask = a.c.page() - 1;
-  const uint4* ks = static_cast<const uint4*>(a.c.k);
-  const uint4* vs = static_cast<const uint4*>(a.c.v);
-  uint4* kd = static_cast<uint4*>(a.c.k);
-  uint4* vd = static_cast<uint4*>(a.c.v);
-  const long long page16 = a.c.page_stride * (a.c.elem == kF32 ? 4 : 2) / 16;
-  const int* from_table = a.c.table + (long long)b * a.c.max_pages;
-  const int* to_table = a.dst_table + (long long)b * a.dst_pages;
-  constexpr int U = 4;
-  for (int j0 = rank * per * U + (tid >> row_shift); j0 < n; j0 += C * per * U) {
-    long long src[U], dst[U];
-    uint4 xk[U], xv[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * per;
-      src[u] = -1;
-      if (j < n) {
-        const int i = __ldcg(kept + j), to = j >> a.c.page_shift;
-        const int sp = from_table[i >> a.c.page_shift], dp = to < a.dst_pages ? to_table[to] : -1;
-        if (sp < 0 || sp >= a.c.n_pages || dp < 0 || dp >= a.c.n_pages) {
-          flag_error(a.c.status, kErrShape);
-        } else {
-          src[u] = sp * page16 + (((long long)g << a.c.page_shift) + (i & mask) << row_shift) + c;
-          dst[u] = dp * page16 + (((long long)g << a.c.page_shift) + (j & mask) << row_shift) + c;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (src[u] >= 0) {
-        xk[u] = ks[src[u]];
-        xv[u] = vs[src[u]];
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (src[u] >= 0) {
-        kd[dst[u]] = xk[u];
-        vd[dst[u]] = xv[u];
-      }
-  }
+  if (rows_here) move_rows(a, row_shift, b, g, n, rank, C);
+}
+
+__global__ void __launch_bounds__(kEvThreads, 2) evict_rows_kernel(EvictArgs a, int row_shift) {
+  pdl_wait();
+  pdl_trigger();
+  move_rows(a, row_shift, blockIdx.z, blockIdx.y, a.lens_out[blockIdx.z], blockIdx.x, gridDim.x);
 }
 
 cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a) {
@@ -574,7 +626,14 @@ cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a) {
   const long long bytes = (long long)std::min(a.keep, a.c.capacity()) * chunks * 16 * 2;
   int C = 1;
   while (C < kEvMaxCluster && units * C * 2 <= 2 * 148 && (bytes > C * (128ll << 10) || a.c.capacity() > C * 2 * kEvThreads)) C *= 2;
-  return launch_cluster(L, evict_paged_kernel, C, dim3((unsigned)(units * C)), dim3(kEvThreads), 0, a, shift);
+  // Fewer CTAs than SMs with much to move: the rows get a grid of their own (4 units of 14191 fp32 rows of 128: 37 us,
+  // 93 where the clusters move them).
+  const bool apart = units * C < 148 && bytes > C * (256ll << 10);
+  const cudaError_t e = launch_cluster(L, evict_paged_kernel, C, dim3((unsigned)(units * C)), dim3(kEvThreads), 0, a, shift, apart ? 0 : 1);
+  if (e != cudaSuccess || !apart) return e;
+  const int at_once = (kEvThreads >> shift) * 4;
+  const int blocks = std::min<long long>((std::min(a.keep, a.c.capacity()) + at_once - 1) / at_once, 4 * 148 / units + 1);
+  return launch_k(L, evict_rows_kernel, dim3(blocks, a.c.Hk, a.c.batch), dim3(kEvThreads), 0, a, shift);
 }
 
 }  // namespace ms
