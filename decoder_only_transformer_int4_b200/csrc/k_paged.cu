@@ -94,13 +94,17 @@ struct alignas(16) Sines {
 
 // Sequence, place and sines of the block's tokens; for all its threads, a barrier at the end.
 __device__ __forceinline__ void rope_tokens(const RopeArgs& a, int t0, int nt, Sines (&cs)[kRopeTokens], TokInfo (&info)[kRopeTokens]) {
-  __shared__ int marks[kRopeTokens];
+  __shared__ int marks[kRopeTokens], place_of[kRopeTokens];   // position to turn by, of live tokens
+  __shared__ bool live_at[kRopeTokens];
   const int tid = threadIdx.x, half = a.rot >> 1;
+  // this thread's pair j of every kstep-th token: its frequency is on the way while the tokens are placed
+  const int wide = half > 1 ? 1 << (32 - __clz(half - 1)) : 1, j = tid & (wide - 1), kstep = kRopeThreads / wide;
+  const double turns = j < half ? a.inv_freq[j] * 0.15915494309189533577 : 0.0;   // per position
   // The sequence of token t: how many row_start[i + 1] are <= t.  Those <= t0 are counted, the others among the
   // block's tokens marked where they end.
   if (tid < kRopeTokens) marks[tid] = 0;
-  int before = 0;
-  for (int i0 = 0; i0 < a.c.batch; i0 += kRopeThreads) before += __syncthreads_count(i0 + tid < a.c.batch && a.row_start[i0 + tid + 1] <= t0);
+  int b = 0;
+  for (int i0 = 0; i0 < a.c.batch; i0 += kRopeThreads) b += __syncthreads_count(i0 + tid < a.c.batch && a.row_start[i0 + tid + 1] <= t0);
   if (nt > 1) {
     for (int i = tid; i < a.c.batch; i += kRopeThreads) {
       const int end = a.row_start[i + 1];
@@ -108,34 +112,25 @@ __device__ __forceinline__ void rope_tokens(const RopeArgs& a, int t0, int nt, S
     }
     __syncthreads();
   }
-  for (int it = tid; it < nt * max(half, 1); it += kRopeThreads) {
-    const int k = it / max(half, 1), j = it - k * max(half, 1);
-    int b = before;
-    for (int i = 1; i <= k; ++i) b += marks[i];
-    const int t = t0 + k;
-    const bool live = b < a.c.batch;   // rows behind the last sequence are left as they were
-    int place = 0, r0 = 0, r1 = 0;
+  int page = -1, place = 0;
+  bool live = false;
+  if (tid < nt) {
+    for (int i = 1; i <= tid; ++i) b += marks[i];
+    live = b < a.c.batch;   // rows behind the last sequence are left as they were
     if (live) {
-      r0 = a.row_start[b];
-      r1 = a.row_start[b + 1];
+      const int t = t0 + tid, r0 = a.row_start[b], r1 = a.row_start[b + 1];
       place = a.c.lens[b] - (r1 - r0) + (t - r0);
+      place_of[tid] = a.positions ? a.positions[t] : place;
+      if (t >= r0 && t < r1 && place >= 0 && place < a.c.capacity())
+        page = a.c.table[(size_t)b * a.c.max_pages + (place >> a.c.page_shift)];   // needed at the end
     }
-    if (j == 0) {
-      long long dst = -1;
-      if (live) {
-        if (t >= r0 && t < r1 && place >= 0 && place < a.c.capacity()) {
-          const int page = a.c.table[(size_t)b * a.c.max_pages + (place >> a.c.page_shift)];
-          if (page >= 0 && page < a.c.n_pages)
-            dst = page * a.c.page_stride + (long long)(place & (a.c.page() - 1)) * a.c.hd;
-        }
-        if (dst < 0) flag_error(a.c.status, kErrShape);
-      }
-      info[k].dst = dst;
-      info[k].live = live;
-    }
-    if (live && half) {
-      const int pos = a.positions ? a.positions[t] : place;
-      const double u = pos * (a.inv_freq[j] * 0.15915494309189533577);   // turns
+    live_at[tid] = live;
+  }
+  __syncthreads();
+#pragma unroll 2
+  for (int k = tid / wide; k < nt; k += kstep) {
+    if (j < half && live_at[k]) {
+      const double u = place_of[k] * turns;
       const double quarter = rint(4.0 * u);
       float s, c;
       sincospif(2.0f * (float)(u - 0.25 * quarter), &s, &c);
@@ -146,11 +141,32 @@ __device__ __forceinline__ void rope_tokens(const RopeArgs& a, int t0, int nt, S
       cs[k].s[j] = sr * a.mscale;
     }
   }
+  if (tid < nt) {
+    long long dst = -1;
+    if (page >= 0 && page < a.c.n_pages) dst = page * a.c.page_stride + (long long)(place & (a.c.page() - 1)) * a.c.hd;
+    if (live && dst < 0) flag_error(a.c.status, kErrShape);
+    info[tid].dst = dst;
+    info[tid].live = live;
+  }
   __syncthreads();
 }
 }  // namespace
 
 namespace {
+// N floats of shared memory, aligned to as many
+template <int N>
+__device__ __forceinline__ void copy_floats(float* to, const float* from) {
+  if constexpr (N == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(from);
+    to[0] = x.x, to[1] = x.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(from + e);
+      to[e] = x.x, to[e + 1] = x.y, to[e + 2] = x.z, to[e + 3] = x.w;
+    }
+  }
+}
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   const float x = a;
   a = x * c - b * s;
@@ -200,20 +216,14 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_paged_kernel(Rope
     if (a.interleaved) {
       n0 = min(max(half - e0 / 2, 0), VEC / 2);
       n1 = min(max(half - e1 / 2, 0), VEC / 2);
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        c[e] = cs[k].c[e0 / 2 + e];
-        s[e] = cs[k].s[e0 / 2 + e];
-        c[VEC / 2 + e] = cs[k].c[e1 / 2 + e];
-        s[VEC / 2 + e] = cs[k].s[e1 / 2 + e];
-      }
+      copy_floats<VEC / 2>(c, cs[k].c + e0 / 2);
+      copy_floats<VEC / 2>(s, cs[k].s + e0 / 2);
+      copy_floats<VEC / 2>(c + VEC / 2, cs[k].c + e1 / 2);
+      copy_floats<VEC / 2>(s + VEC / 2, cs[k].s + e1 / 2);
     } else if (i < turned) {
       n0 = VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        c[e] = cs[k].c[e0 + e];
-        s[e] = cs[k].s[e0 + e];
-      }
+      copy_floats<VEC>(c, cs[k].c + e0);
+      copy_floats<VEC>(s, cs[k].s + e0);
     }
     if (!mine || !info[k].live) return;
     for (int h1 = h0; h1 < heads; h1 += U * head_groups) {
