@@ -76,7 +76,7 @@ __device__ __forceinline__ void pack(Pack<__nv_bfloat16, N>& p, const float (&y)
 // out once for all heads.  A thread then has the same two chunks of 16 bytes in every so-manyth head of its
 // token, so that its sines stay in registers (read from shared memory for each head, their bank conflicts and
 // loads held bf16 rows to half the bandwidth).  32767 rows of 40 heads of 64, fp32 to fp16: 98 us, 6.2 TB/s;
-// 4132 rows of 48 bf16 heads of 128: 25 us, 4.0 TB/s (the chain and the last wave show); 64 rows: 3.2 us.
+// 4132 rows of 48 bf16 heads of 128: 26 us, 3.9 TB/s (the chain at the start shows); 64 rows: 3.1 us.
 // ---------------------------------------------------------------------------------
 namespace {
 constexpr int kRopeThreads = 256, kRopeTokens = 32, kRopeItems = 2;
@@ -316,6 +316,11 @@ static cudaError_t rope_go(const Launch& L, const RopeArgs& a) {
   int tokens = 1;
   const int items = ((a.q ? a.H : 0) + 2 * a.c.Hk) * a.c.hd / (vector ? 2 * VEC : 2), most = std::min(kRopeTokens, kRopeThreads * 2 * VEC / a.c.hd);
   while (tokens < most && a.rows >= 148 * 2 * 2 * tokens && (tokens * items < 2 * kRopeThreads || (tokens < 8 && a.rows >= 148 * 6 * 2 * tokens))) tokens *= 2;
+  // or as many as make one wave of all blocks, each with 24 items a thread at most (3000 rows of 72 heads: 20.4 us at 8, 22.6
+  // at 2)
+  int wave = 1;
+  while (wave < most && a.rows > (long long)148 * 4 * wave) wave *= 2;
+  if (a.rows <= (long long)148 * 4 * wave && wave * items <= 24 * kRopeThreads) tokens = std::max(tokens, wave);
   const dim3 grid((a.rows + tokens - 1) / tokens), block(kRopeThreads);
   if (vector) return launch_k(L, rope_append_paged_kernel<QT, KT, true>, grid, block, 0, a, tokens);
   return launch_k(L, rope_append_paged_kernel<QT, KT, false>, grid, block, 0, a, tokens);
