@@ -76,10 +76,10 @@ __device__ __forceinline__ void pack(Pack<__nv_bfloat16, N>& p, const float (&y)
 // out once for all heads.  A thread then has the same two chunks of 16 bytes in every so-manyth head of its
 // token, so that its sines stay in registers (read from shared memory for each head, their bank conflicts and
 // loads held bf16 rows to half the bandwidth).  32767 rows of 40 heads of 64, fp32 to fp16: 98 us, 6.2 TB/s;
-// 4132 rows of 48 bf16 heads of 128: 26 us, 3.9 TB/s (the chain at the start shows); 64 rows: 3.1 us.
+// 4132 rows of 48 bf16 heads of 128: 21.8 us, 4.7 TB/s (the chain at the start shows); 64 rows: 3.1 us.
 // ---------------------------------------------------------------------------------
 namespace {
-constexpr int kRopeThreads = 256, kRopeTokens = 32, kRopeItems = 2;
+constexpr int kRopeThreads = 256, kRopeTokens = 32;
 
 struct TokInfo {
   long long dst;   // element offset of kv head 0's row in the pages, -1: not appended
@@ -199,7 +199,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_paged_kernel(Rope
     constexpr int VEC = 16 / sizeof(QT);
     using In = Pack<QT, VEC>;
     using Out = Pack<KT, VEC>;
-    constexpr int U = kRopeItems;
+    // 16-bit chunks hold twice the elements: a second one at once would not fit 64 registers beside the sines (four blocks
+    // an SM; 4132 bf16 rows of 48 heads: 26.1 us, 21.8 with one)
+    constexpr int U = sizeof(QT) == 2 ? 1 : 2;
     // a thread has the same two chunks of every head_groups-th head of one token, and their sines in registers
     const int shift = hd == 64 ? (VEC == 4 ? 3 : 2) : (VEC == 4 ? 4 : 3);   // 2^shift pairs of chunks in a head
     const int i = tid & ((1 << shift) - 1), head_groups = (kRopeThreads >> shift) / tokens;   // tokens: a power of two
@@ -316,8 +318,8 @@ static cudaError_t rope_go(const Launch& L, const RopeArgs& a) {
   int tokens = 1;
   const int items = ((a.q ? a.H : 0) + 2 * a.c.Hk) * a.c.hd / (vector ? 2 * VEC : 2), most = std::min(kRopeTokens, kRopeThreads * 2 * VEC / a.c.hd);
   while (tokens < most && a.rows >= 148 * 2 * 2 * tokens && (tokens * items < 2 * kRopeThreads || (tokens < 8 && a.rows >= 148 * 6 * 2 * tokens))) tokens *= 2;
-  // or as many as make one wave of all blocks, each with 24 items a thread at most (3000 rows of 72 heads: 20.4 us at 8, 22.6
-  // at 2)
+  // or as many as make one wave of all blocks, each with 24 items a thread at most (3000 rows of 72 heads: 10% faster at 8
+  // than at 2)
   int wave = 1;
   while (wave < most && a.rows > (long long)148 * 4 * wave) wave *= 2;
   if (a.rows <= (long long)148 * 4 * wave && wave * items <= 24 * kRopeThreads) tokens = std::max(tokens, wave);

@@ -360,7 +360,8 @@ typedef enum { MS_ELEM_F32 = 0, MS_ELEM_F16 = 1, MS_ELEM_BF16 = 2 } ms_elem;
  * aligned, page_stride a multiple of 16 bytes; else MS_ERR_SHAPE or MS_ERR_INVALID_ARG.
  * status (may be NULL): a device word that calls set bits in, see ms_op_status.  A length, row range or
  * page outside its limits is device data: the kernels check it, touch nothing outside the
- * buffers, leave that sequence's rows out and set a bit. */
+ * buffers, leave that sequence's rows out (in the attention, a page out of range counts as zeros) and set a
+ * bit. */
 typedef struct {
   void* k;
   void* v;
