@@ -185,15 +185,16 @@ __global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a,
     const int step = (hi - lo + 31) / 32;
     const int w0 = min((long long)hi, lo + (long long)lane * step), w1 = min(hi, w0 + step);
     double part[2] = {0.0, 0.0};
-    for (int w = w0; w < w1; w += U) {
-      float pv[U], qv[U];
+    constexpr int N = 4;   // little code: one warp runs it, once, and waits for every line of it
+    for (int w = w0; w < w1; w += N) {
+      float pv[N], qv[N];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
+      for (int k = 0; k < N; ++k) {
         pv[k] = w + k < w1 ? p[w + k] : 0.f;
         qv[k] = q && w + k < w1 ? q[w + k] : 0.f;
       }
 #pragma unroll
-      for (int k = 0; k < U; ++k) part[k & 1] += w + k == banned ? 0.0 : fmax((double)pv[k] - (double)qv[k], 0.0);
+      for (int k = 0; k < N; ++k) part[k & 1] += w + k == banned ? 0.0 : fmax((double)pv[k] - (double)qv[k], 0.0);
     }
     const double y = part[0] + part[1], c = at + warp_scan_d(y, lane);
     const unsigned over = __ballot_sync(0xffffffffu, y > 0.0 && c > goal);
