@@ -16,8 +16,9 @@
 // sums into all CTAs of the cluster, so that one cluster barrier is the only wait; the warp whose run
 // holds the border then narrows it 32 times at a step (each lane sums a contiguous piece, it is in L1 or L2
 // by then) instead of walking it.  Walked 32 values a step, the border cost more than all else: 18.6 us for
-// 64 sequences of 32003 tokens and 26.9 us for 32 of 100003, against 8.0 us and
-// 10.7 us (4.8 us for one sequence of 1393 tokens; half the threads, or half the CTAs: 10% to 30% more).
+// 64 sequences of 32003 tokens and 26.9 us for 32 of 100003, against 7.4 us and 8.3 us (4.5 us for one sequence of
+// 1393 tokens).  512 threads a CTA (with half the threads, or half the CTAs: 10% to 30% more) and 64 registers, two CTAs an
+// SM: with fewer the loads of a round do not fit (40 registers: 9.4 and 10.1 us).
 #include <cooperative_groups.h>
 #include <math.h>
 #include "ms_device.cuh"
@@ -45,7 +46,7 @@ __device__ __forceinline__ double warp_scan_d(double v, int lane) {
 }
 }  // namespace
 
-__global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a, unsigned* status) {
+__global__ void __launch_bounds__(kVerThreads, 2) verify_draft_kernel(VerifyArgs a, unsigned* status) {
   namespace cg = cooperative_groups;
   __shared__ int first_refused;
   __shared__ double sums[kVerRuns];   // of the runs of the whole cluster
@@ -209,9 +210,10 @@ __global__ void __launch_bounds__(kVerThreads) verify_draft_kernel(VerifyArgs a,
 }
 
 cudaError_t launch_verify_draft(const Launch& L, const VerifyArgs& a) {
-  // a CTA for each 8192 tokens of the row (16 a thread: one or two rounds of loads), up to a portable cluster
+  // a CTA for each 8192 tokens of the row (16 a thread: one or two rounds of loads), up to a portable cluster and to two an
+  // SM in all (43 sequences of 72091: 13.1 us in clusters of 4, 15.2 in more than fit at once)
   int C = 1;
-  while (C < kVerMaxCluster && C * 8192 < a.V) C *= 2;
+  while (C < kVerMaxCluster && C * 8192 < a.V && (long long)a.batch * C * 2 <= 2 * 148) C *= 2;
   return launch_cluster(L, verify_draft_kernel, C, dim3(a.batch * C), dim3(kVerThreads), 0, a, L.status);
 }
 
