@@ -92,6 +92,12 @@ struct alignas(16) Sines {
   float c[64], s[64];
 };
 
+// A sequence whose rows can be appended: its range lies in the call's rows, its length in the table, and it holds its rows.
+// Only such a one is touched at all, as in the attention; a range that is cut off would put rows in places of older ones.
+__device__ __forceinline__ bool rope_sequence_ok(const RopeArgs& a, int r0, int r1, int T) {
+  return r0 >= 0 && r0 <= r1 && r1 <= a.rows && T <= a.c.capacity() && r1 - r0 <= T;
+}
+
 // Sequence, place and sines of the block's tokens; for all its threads, a barrier at the end.
 __device__ __forceinline__ void rope_tokens(const RopeArgs& a, int t0, int nt, Sines (&cs)[kRopeTokens], TokInfo (&info)[kRopeTokens]) {
   __shared__ int marks[kRopeTokens], place_of[kRopeTokens];   // position to turn by, of live tokens
@@ -104,7 +110,14 @@ __device__ __forceinline__ void rope_tokens(const RopeArgs& a, int t0, int nt, S
   // block's tokens marked where they end.
   if (tid < kRopeTokens) marks[tid] = 0;
   int b = 0;
-  for (int i0 = 0; i0 < a.c.batch; i0 += kRopeThreads) b += __syncthreads_count(i0 + tid < a.c.batch && a.row_start[i0 + tid + 1] <= t0);
+  for (int i0 = 0; i0 < a.c.batch; i0 += kRopeThreads) {
+    const int i = i0 + tid;
+    const bool is = i < a.c.batch;
+    const int end = is ? a.row_start[i + 1] : 0;
+    // the first block flags the sequences that are left out, whether they have rows or not
+    if (blockIdx.x == 0 && is && !rope_sequence_ok(a, a.row_start[i], end, a.c.lens[i])) flag_error(a.c.status, kErrShape);
+    b += __syncthreads_count(is && end <= t0);
+  }
   if (nt > 1) {
     for (int i = tid; i < a.c.batch; i += kRopeThreads) {
       const int end = a.row_start[i + 1];
@@ -116,13 +129,13 @@ __device__ __forceinline__ void rope_tokens(const RopeArgs& a, int t0, int nt, S
   bool live = false;
   if (tid < nt) {
     for (int i = 1; i <= tid; ++i) b += marks[i];
-    live = b < a.c.batch;   // rows behind the last sequence are left as they were
-    if (live) {
-      const int t = t0 + tid, r0 = a.row_start[b], r1 = a.row_start[b + 1];
-      place = a.c.lens[b] - (r1 - r0) + (t - r0);
+    if (b < a.c.batch) {
+      const int t = t0 + tid, r0 = a.row_start[b], r1 = a.row_start[b + 1], T = a.c.lens[b];
+      place = T - (r1 - r0) + (t - r0);
       place_of[tid] = a.positions ? a.positions[t] : place;
-      if (t >= r0 && t < r1 && place >= 0 && place < a.c.capacity())
-        page = a.c.table[(size_t)b * a.c.max_pages + (place >> a.c.page_shift)];   // needed at the end
+      // rows before the first sequence and behind the last, and those of a sequence that is left out, stay as they were
+      live = rope_sequence_ok(a, r0, r1, T) && t >= r0 && t < r1;
+      if (live) page = a.c.table[(size_t)b * a.c.max_pages + (place >> a.c.page_shift)];   // needed at the end
     }
     live_at[tid] = live;
   }

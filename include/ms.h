@@ -387,8 +387,10 @@ ms_status ms_op_status(uint32_t* status, void* stream);
 /* Rotary positions of new q and k rows and the append of k and v to the cache.
  * The rows of the batch are packed: sequence b has rows row_start[b] .. row_start[b+1] - 1
  * (int32 [batch + 1], not decreasing, row_start[batch] <= rows) and they are its last positions,
- * so row r goes to position lens[b] - row_start[b+1] + r.  Rows behind row_start[batch] are left as they
- * were.  q [rows][n_heads][head_dim], k and v [rows][n_kv_heads][head_dim] of q_elem at row strides
+ * so row r goes to position lens[b] - row_start[b+1] + r.  Rows before row_start[0] and behind row_start[batch]
+ * are left as they were, and so are those of a sequence whose range or length is out of its limits (flagged; more rows than
+ * positions among them): neither the pages nor q_out change.  A row whose page is out of range is turned but not
+ * appended (flagged).  q [rows][n_heads][head_dim], k and v [rows][n_kv_heads][head_dim] of q_elem at row strides
  * ldq, ldk, ldv (elements: the parts of a fused QKV row are passed in place).  Pair j < rotary_dim / 2 of
  * each q and k head, elements (j, j + rotary_dim / 2) or with interleaved (2j, 2j + 1), turns:
  *     (a, c) -> ((a cos t - c sin t) * mscale, (a sin t + c cos t) * mscale),

@@ -1,0 +1,76 @@
+"""The paged-cache operators at the edges of what they take."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as R
+
+pytestmark = pytest.mark.gpu
+ms = pytest.importorskip("decoder_only_transformer_int4_b200")
+
+
+def _same(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ---- the append leaves out what the attention leaves out --------------------------------------
+
+BAD_RANGES = {
+    # name: (lens, row_start, sequences left out, rows of no sequence)
+    "past the rows": ([40, 40, 40], [0, 2, 4, 9], [2], []),
+    "past the rows, from a row that is not there": ([40, 40, 40], [0, 2, 6, 9], [2], []),
+    "decreasing": ([40, 40, 40], [0, 4, 3, 6], [1], []),
+    "negative": ([40, 40, 40], [-2, 2, 4, 6], [0], []),
+    "rows before the first sequence": ([40, 40, 40], [2, 3, 4, 6], [], [0, 1]),
+    "length past the capacity": ([40, 50, 40], [0, 2, 4, 6], [1], []),
+    "length below zero": ([40, -1, 40], [0, 2, 4, 6], [1], []),
+    "more rows than positions": ([40, 2, 40], [0, 1, 4, 6], [1], []),
+    "length past the capacity of a sequence without rows": ([40, 50, 40], [0, 3, 3, 6], [1], []),
+}
+
+
+@pytest.mark.parametrize("kq,kkv", R.PAIRS)
+@pytest.mark.parametrize("case", list(BAD_RANGES))
+@pytest.mark.parametrize("heads,skew", [(4, 0), (4, 1), (0, 0)])
+def test_append_leaves_out_bad_sequences(kq, kkv, case, heads, skew):
+    lens, start, bad, loose = BAD_RANGES[case]
+    hk, hd, rows = 2, 64, 6
+    pages = R.Pages([40, 40, 40], hk, 16, hd, kkv, seed=401)         # 3 pages each: 48 positions
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = pages.cuda(ms, status, lens=lens)
+    k0, v0 = pages.dk.clone(), pages.dv.clone()
+    g = torch.Generator().manual_seed(402)
+    buf = torch.randn((rows, (heads + 2 * hk) * hd + skew), generator=g).to(R.TYPES[kq]).cuda()
+    x = buf.as_strided((rows, heads + 2 * hk, hd), (buf.shape[1], hd, 1), skew)
+    f = torch.tensor([1e4 ** (-2 * j / hd) for j in range(hd // 2)], dtype=torch.float64)
+    out = torch.full((rows, heads, hd), 7.0, dtype=x.dtype, device="cuda") if heads else None
+    ms.rope_append_paged(kv, x[:, :heads] if heads else None, x[:, heads:heads + hk], x[:, heads + hk:],
+                         torch.tensor(start, dtype=torch.int32).cuda(), f.cuda(), out=out)
+    if bad:
+        with pytest.raises(ms.MsError) as e:
+            ms.op_status(status)
+        assert e.value.status == ms.MS_ERR_SHAPE
+    else:
+        ms.op_status(status)
+    # a row belongs to the sequence whose end is the first behind it
+    at = {}
+    for t in range(rows):
+        b = sum(s <= t for s in start[1:])
+        if b < 3 and b not in bad and t >= start[b]:
+            at[t] = (b, lens[b] - (start[b + 1] - start[b]) + t - start[b])
+    assert not set(at) & set(loose)
+    xs = R.f64(x)
+    for t, (b, pos) in at.items():
+        want = R.rotate(xs[t:t + 1, :heads + hk], [pos], f.numpy(), False, 1.0)[0]
+        p, i = int(pages.table[b, pos // 16]), pos % 16
+        mag = np.sqrt((xs[t, :heads + hk] ** 2).sum(-1, keepdims=True))
+        # as in test_paged_gpu.py: sines, products and the sum are off by 8 * 2^-24 of the pair's size, then one rounding
+        tol = lambda kind, y, m: R.half_step(kind) * np.abs(y) + 8 * 2.0 ** -24 * m + (2.0 ** -25 if kind == "f16" else 0)  # noqa: E731
+        assert np.all(np.abs(R.f64(pages.dk[p, :, i]) - want[heads:]) <= tol(kkv, want[heads:], mag[heads:]))
+        assert np.array_equal(R.f64(pages.dv[p, :, i]), R.f64(x[t, heads + hk:].to(R.TYPES[kkv])))
+        if heads:
+            assert np.all(np.abs(R.f64(out[t]) - want[:heads]) <= tol(kq, want[:heads], mag[:heads]))
+        pages.dk[p, :, i], pages.dv[p, :, i] = k0[p, :, i], v0[p, :, i]
+    assert _same(pages.dk, k0) and _same(pages.dv, v0)              # nothing else was written
+    if heads:
+        assert all(bool((out[t] == 7.0).all()) for t in range(rows) if t not in at)
