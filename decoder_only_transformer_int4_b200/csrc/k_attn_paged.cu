@@ -481,11 +481,12 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
 #pragma unroll
             for (int k = 0; k < HD / 32; ++k) top = fmaxf(top, fabsf(x[k]));
             top = warp_max(top);
-            // the row's largest element to [2^13, 2^14): its half keeps 11 bits and its rest 11 more
+            // the row's largest element to [2^13, 2^14): its half keeps 11 bits and its rest 11 more.  Subnormal ones go
+            // up by 2^126 (what is left of their bits fits the pair then, too), so that 2^-e stays a normal number.
             if (top > 0.f && top < INFINITY) {
               int e;
               frexpf(top, &e);
-              e = max(-100, min(100, 14 - e));
+              e = min(126, 14 - e);
               up = ldexpf(1.f, e);
               f = a.scale2 * ldexpf(1.f, -e);
             }

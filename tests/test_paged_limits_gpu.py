@@ -8,6 +8,8 @@ import paged_ref as R
 pytestmark = pytest.mark.gpu
 ms = pytest.importorskip("decoder_only_transformer_int4_b200")
 
+U = 2.0 ** -23
+
 
 def _same(a, b):
     return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
@@ -74,3 +76,23 @@ def test_append_leaves_out_bad_sequences(kq, kkv, case, heads, skew):
     assert _same(pages.dk, k0) and _same(pages.dv, v0)              # nothing else was written
     if heads:
         assert all(bool((out[t] == 7.0).all()) for t in range(rows) if t not in at)
+
+
+# ---- fp32 queries on a half cache ---------------------------------------------------------------
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 126, 2.0 ** 118, 2.0 ** -105, 2.0 ** -126])
+def test_attention_of_queries_at_the_ends_of_fp32(hd, size):
+    # powers of two: the scores are those of the unscaled queries
+    pages = R.Pages([200, 70], 1, 16, hd, "f16", seed=411)
+    g = torch.Generator().manual_seed(412)
+    q = torch.rand((3, 2, hd), generator=g) * 2 - 1                    # below 2 in size: q * size below 2^127
+    big = (q * size).cuda()
+    x = big.cpu().double().numpy() / size                              # what is left of them where they are subnormal
+    scale = 2.0 / size if size <= 2.0 ** 126 else None
+    got = R.f64(ms.attn_paged(pages.cuda(ms), big, R.starts([1, 2]).cuda(), 2, scale=scale))
+    ref, A, spread, _ = R.attention(pages, torch.from_numpy(x), [1, 2], 2.0)
+    T = np.array([200, 70, 70])[:, None]
+    # as in test_paged_gpu.py: (hd + 16) U of the products' sum for a score, 2^-21 for the pairs, 2 T U for the sums
+    tol = R.half_step("f32") * np.abs(ref) + A * (2 * (hd + 17) * U * spread + 8 * U + 2.0 ** -21 + 2 * T * U)[..., None]
+    assert np.all(np.abs(got - ref) <= tol), np.abs(got - ref).max()
