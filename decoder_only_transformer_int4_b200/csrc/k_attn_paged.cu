@@ -34,8 +34,11 @@
 // cannot hide a step's chain of loads, products and exponentials (drafted rows: 211 us).
 //
 // Arithmetic.  16-bit caches: products of m16n8k16 with fp32 sums; the probabilities enter P V as a
-// 16-bit pair hi + lo (two MMAs), so that they carry 16 (bf16) or 22 (fp16) bits and not 8 or 11: the
-// error of the result is then the rounding of its store.  fp32 queries on a half cache enter as a pair
+// 16-bit pair hi + lo (two MMAs), so that they carry 16 (bf16) or up to 22 (fp16) bits and not 8 or 11: the
+// error of the result is then the rounding of its store.  fp16 pairs have a range: where the result is fp16, too, what
+// is lost of a probability is at most 2^-35 of its row's largest (so one below that counts as 0, which shows where the v of
+// all larger ones are next to 0); where it is fp32, small probabilities are brought into the range by powers of two, step by
+// step, and keep their 22 bits whatever leads them.  fp32 queries on a half cache enter as a pair
 // too, after an exact power-of-two scale of the row.  fp32 caches: m16n8k8 tf32 with every operand as a
 // pair of 11-bit halves, three products (hi hi, hi lo, lo hi): ~2^-21 per product.  Running maximum and
 // sum in fp32, in the exponent's base 2.  Where the result is stored in fp32, each step's P V is summed
@@ -87,10 +90,14 @@ struct Kargs {
   int slices;                       // CTAs that join a unit's pieces
 };
 
-// The exponent of every probability is raised by this where P enters as fp16 pairs, so that one of
-// 2^-20 keeps its lo half; it cancels in o / l.
+// The exponent of every probability is raised by this where P enters as fp16 pairs, so that fewer of them fall
+// among the subnormal halves; it cancels in o / l.
 template <typename KT>
 constexpr float bias_of() { return std::is_same<KT, __half>::value ? 10.f : 0.f; }
+// fp32 results from a half cache: lo enters 2^12 times as large and its sum is scaled back.  The pair of a probability from
+// 2^-14 to 2^14 (the normal halves) is then off by 2^-22 of it: lo's step of 2^-24 counts 2^-36.  Smaller ones are brought
+// into that range before.  64 streams 19.8 us, 19.2 without; 32 sequences with 5 rows of 16 heads 41.8 us, 39.6 without.
+constexpr float kLoUp = 4096.f, kPairFrom = 0x1p-14f;
 // How far a score may pass the running reference before sums are scaled anew: probabilities stay below 2^14
 constexpr float kSlack = 4.f;
 
@@ -130,6 +137,15 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// two fp32 multiplications, or multiplications and additions, in one instruction: (a, b) *= f, and (a, b) += (x, y) * (f, g)
+__device__ __forceinline__ void mul2(float& a, float& b, float f) {
+  asm("{.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;}"
+      : "+f"(a), "+f"(b) : "f"(f));
+}
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float f, float g) {
+  asm("{.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %5};\n\tfma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;}"
+      : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(f), "f"(g));
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -401,6 +417,31 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
   auto load_q = [&](uint32_t (&t)[4], int nb, int ks, int plane) {
     const int r = nb * 8 + (lane & 7), c = 2 * ks + (lane >> 3);
     ldsm4(t, smem_u32(qs) + (plane * R * HD + r * HD + ((c ^ (r & 7)) << 3)) * 2);
+  };
+
+  // The transposed fragments of V's elements 16 md .. 16 md + 31 of the staged step.
+  auto load_v = [&](uint32_t (&va)[2][4], uint32_t vu, int md) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = (lane & 7) + 8 * (lane >> 4), c = 2 * (md + u) + ((lane >> 3) & 1);
+      ldsm4t(va[u], vu + r * S::kRowBytes + swz_v<false>(c, r) * 16);
+    }
+  };
+  // Probabilities as B fragments (positions 2 t4, 2 t4 + 1 (+ 8 i) of row g8), hi and what it leaves
+  auto pairs = [&](const float (&p)[NB][4], uint32_t (&ph)[NB][2], uint32_t (&pl)[NB][2]) {
+    if constexpr (!F32) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float ra, rb, za, zb;
+          const uint32_t h = Two<KT>::pack(p[nb][2 * i], p[nb][2 * i + 1], ra, rb);
+          if constexpr (Q32) mul2(ra, rb, kLoUp);
+          const uint32_t w = Two<KT>::pack(ra, rb, za, zb);
+          ph[nb][i] = transpose8(h);
+          pl[nb][i] = transpose8(w);
+        }
+    }
   };
 
   // A unit's sequence and query rows (one warp, every fourth row), read before they are needed: ahead of the first
@@ -722,28 +763,15 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
                 if (d.pos0 + r < lim[nb][k & 1]) O[nb][md][k] = fmaf(p[k & 1], x, O[nb][md][k]);
               }
           }
-      } else if constexpr (!F32) {
-        uint32_t ph[NB][2], pl[NB][2];
+      } else if constexpr (Q32) {
+        auto add = [&](const float (&p)[NB][4], const float (&down)[NB][2]) {
+          uint32_t ph[NB][2], pl[NB][2];
+          pairs(p, ph, pl);
+          // two tiles of elements at a time: products that add to one sum stay 2 NB apart
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float ra, rb, za, zb;
-            const uint32_t h = Two<KT>::pack(sc[nb][2 * i], sc[nb][2 * i + 1], ra, rb);
-            const uint32_t w = Two<KT>::pack(ra, rb, za, zb);
-            ph[nb][i] = transpose8(h);   // positions 2 t4, 2 t4 + 1 (+ 8 i) of row g8: a B fragment
-            pl[nb][i] = transpose8(w);
-          }
-        // two tiles of elements at a time: products that add to one sum stay 2 NB apart
-#pragma unroll
-        for (int md = 0; md < MD; md += 2) {
-          uint32_t va[2][4];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int r = (lane & 7) + 8 * (lane >> 4), c = 2 * (md + u) + ((lane >> 3) & 1);
-            ldsm4t(va[u], vu + r * S::kRowBytes + swz_v<false>(c, r) * 16);
-          }
-          if constexpr (Q32) {
+          for (int md = 0; md < MD; md += 2) {
+            uint32_t va[2][4];
+            load_v(va, vu, md);
             float x[2][NB][4];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -756,23 +784,77 @@ __global__ void __launch_bounds__(kThreads) attn_paged_kernel(Kargs a) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16<KT>(x[u][nb], va[u], ph[nb][0], ph[nb][1]);
+              for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) mul2(x[u][nb][k], x[u][nb][k + 1], 1.f / kLoUp);
+                mma16<KT>(x[u][nb], va[u], ph[nb][0], ph[nb][1]);
+              }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) O[nb][md + u][k] += x[u][nb][k];
-          } else {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16<KT>(O[nb][md + u], va[u], ph[nb][0], ph[nb][1]);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16<KT>(O[nb][md + u], va[u], pl[nb][0], pl[nb][1]);
+                for (int k = 0; k < 4; k += 2)
+                  fma2(O[nb][md + u][k], O[nb][md + u][k + 1], x[u][nb][k], x[u][nb][k + 1], down[nb][0], down[nb][1]);
           }
+        };
+        unsigned smallest = 0xffffffffu;   // the smallest but 0, by its bits (one less, so that 0 comes last)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) smallest = min(smallest, __float_as_uint(sc[nb][k]) - 1u);
+        float down[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) down[nb][0] = down[nb][1] = 1.f;
+        if (!__any_sync(0xffffffffu, smallest < __float_as_uint(kPairFrom) - 1u)) {
+          add(sc, down);
+        } else {
+          // Probabilities that a pair does not hold: each row's largest is brought to [2^9, 2^10) by a power of two, what then
+          // is in the pair's range is added and taken out, until nothing is left (each pass takes 23 powers of two).
+          bool left = true;
+#pragma unroll 1
+          while (left) {
+            float p[NB][4];
+            left = false;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float top = fmaxf(sc[nb][k], sc[nb][2 + k]);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                const unsigned e = max(10u, __float_as_uint(top) >> 23 & 255u);   // 2^126 at most; both factors are normal
+                const float up = __uint_as_float((263 - e) << 23);
+                down[nb][k] = __uint_as_float((e - 9) << 23);
+#pragma unroll
+                for (int i = k; i < 4; i += 2) {
+                  const float y = sc[nb][i] * up;
+                  const bool now = !(y < kPairFrom);   // NaN too
+                  p[nb][i] = now ? y : 0.f;
+                  sc[nb][i] = now ? 0.f : sc[nb][i];
+                  left |= sc[nb][i] >= 0x1p-126f;   // ex2 gives no smaller ones, and one would never come into the range
+                }
+              }
+            add(p, down);
+            left = __any_sync(0xffffffffu, left);
+          }
+        }
+      } else if constexpr (!F32) {
+        uint32_t ph[NB][2], pl[NB][2];
+        pairs(sc, ph, pl);
+#pragma unroll
+        for (int md = 0; md < MD; md += 2) {   // as above
+          uint32_t va[2][4];
+          load_v(va, vu, md);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16<KT>(O[nb][md + u], va[u], ph[nb][0], ph[nb][1]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16<KT>(O[nb][md + u], va[u], pl[nb][0], pl[nb][1]);
         }
       } else {
         // k index t is position 8 nt + 2 t, t + 4 the one after it

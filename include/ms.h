@@ -424,7 +424,9 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
  * weights (may be NULL): fp32 [batch][n_kv_heads][ldw], ldw >= max_pages * page_size: position t's entry
  * grows by the sum of p_t over the rows and the heads of its group (for ms_op_evict_paged).
  * The types are those of ms_op_rope_append_paged.  Scores, softmax and sums are fp32 (fp32 operands enter as pairs
- * of 11-bit halves, probabilities as pairs of 16-bit halves); rounded once at the store.  The
+ * of 11-bit halves, probabilities as pairs of 16-bit halves); rounded once at the store.  With fp16 rows up to
+ * 2^-35 of its row's largest is lost of a probability, so that one below that may count as 0; with the other types
+ * they keep 16 bits (bf16) or 21 and more, however far one position leads the others.  The
  * result of a sequence does not depend on timing, but its rounding on how the batch's work is split.
  * workspace: ms_op_attn_paged_workspace bytes (0 for arguments that the call refuses), 256-byte
  * aligned, holding nothing before or after; calls that may overlap on the GPU need their own, and their own weights.

@@ -96,3 +96,31 @@ def test_attention_of_queries_at_the_ends_of_fp32(hd, size):
     # as in test_paged_gpu.py: (hd + 16) U of the products' sum for a score, 2^-21 for the pairs, 2 T U for the sums
     tol = R.half_step("f32") * np.abs(ref) + A * (2 * (hd + 17) * U * spread + 8 * U + 2.0 ** -21 + 2 * T * U)[..., None]
     assert np.all(np.abs(got - ref) <= tol), np.abs(got - ref).max()
+
+
+@pytest.mark.parametrize("kq,kkv", [("f32", "f16"), ("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("T", [9, 16, 200, 1500])
+@pytest.mark.parametrize("nats", [10, 17, 24, 30, 45, 70])
+@pytest.mark.parametrize("group", [1, 12, 28])
+def test_attention_where_the_heaviest_position_holds_nothing(kq, kkv, hd, T, nats, group):
+    """One position leads all others by `nats` and its v is 0: the result is made of probabilities e^-nats and below alone."""
+    pages = R.Pages([T], 1, 16, hd, kkv, seed=421)
+    g = torch.Generator().manual_seed(422)
+    lead = T // 3
+    for i in range(T):
+        p, j = int(pages.table[0, i // 16]), i % 16
+        pages.k[p, 0, j] = 0.0
+        # multiples of 1/4 below 16: exact in every type, and so are the scores before the factor log2 e
+        pages.k[p, 0, j, 0] = 0.0 if i == lead else -nats - 0.25 * int(torch.randint(0, 16, (1,), generator=g))
+        if i == lead:
+            pages.v[p, 0, j] = 0.0
+    q = torch.zeros((1, group, hd))
+    q[..., 0] = 1.0
+    q = q.to(R.TYPES[kq])
+    got = R.f64(ms.attn_paged(pages.cuda(ms), q.cuda(), R.starts([1]).cuda(), 1, scale=1.0))
+    ref, A, spread, _ = R.attention(pages, q, [1], 1.0)
+    # a score's exact product takes two roundings (the factor and the product, 2^-24 each) and a third where the reference is
+    # subtracted, so a probability is off by 2 * 3/2 U |s|; exp2 4 U above and below; the pairs 2^-21 or 2^-17; two sums of T
+    tol = R.half_step(kq) * np.abs(ref) + A * (3 * U * spread + 8 * U + (2.0 ** -17 if kkv == "bf16" else 2.0 ** -21) + 2 * T * U)[..., None]
+    assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / np.maximum(A, 1e-300)).max()
