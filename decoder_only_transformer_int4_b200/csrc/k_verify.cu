@@ -31,6 +31,8 @@ namespace {
 constexpr int kVerThreads = 512, kVerWarps = kVerThreads / 32, kVerMaxCluster = 8;
 constexpr int kVerRuns = kVerMaxCluster * kVerWarps, kPerLane = kVerRuns / 32;
 
+// max(d, 0), but NaN where d is: a row that holds one has no sum
+__device__ __forceinline__ double rest(double d) { return d <= 0.0 ? 0.0 : d; }
 __device__ __forceinline__ double warp_sum_d(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_draft_kernel(VerifyArgs
           qv[k] = in ? q[v + 32 * k] : 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k) s[k & 3] += fmax((double)pv[k] - (double)qv[k], 0.0);
+        for (int k = 0; k < U; ++k) s[k & 3] += rest((double)pv[k] - (double)qv[k]);
       }
     } else {
       for (int v = v0 + lane; v < v1; v += 64 * U) {
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_draft_kernel(VerifyArgs
     }
     incl = warp_scan_d(mine, lane);
     total = __shfl_sync(0xffffffffu, incl, 31);
-    if (total > 0.0 || !(q || banned >= 0)) break;
+    if (!(total <= 0.0) || !(q || banned >= 0)) break;   // NaN is refused below
     q = nullptr;   // the whole cluster: p itself
     banned = -1;
     cluster.sync();   // the sums have been read
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_draft_kernel(VerifyArgs
         qv[k] = q && w + k < w1 ? q[w + k] : 0.f;
       }
 #pragma unroll
-      for (int k = 0; k < N; ++k) part[k & 1] += w + k == banned ? 0.0 : fmax((double)pv[k] - (double)qv[k], 0.0);
+      for (int k = 0; k < N; ++k) part[k & 1] += w + k == banned ? 0.0 : rest((double)pv[k] - (double)qv[k]);
     }
     const double y = part[0] + part[1], c = at + warp_scan_d(y, lane);
     const unsigned over = __ballot_sync(0xffffffffu, y > 0.0 && c > goal);

@@ -464,8 +464,8 @@ ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t
  * u_sample[b] times the total.  Products and sums in double.
  * accepted int32 [batch]; out int32 [batch][max_draft + 1]: the accepted drafts, the next token, -1 behind.
  * Probabilities are finite and not negative (they need not sum to 1), random numbers in [0, 1).  A token outside
- * [0, vocab) is refused, a row that sums to nothing (or not to a finite number) or a u_sample outside [0, 1) gives the
- * next token -1; all flag status (may be NULL), as does a row range out of its limits (nothing accepted, every token -1). */
+ * [0, vocab) is refused, weights to draw from (p_n, or what q_i leaves of p_i) that sum to nothing or not to a finite
+ * number, or a u_sample outside [0, 1), give the next token -1; all flag status (may be NULL), as does a row range out of its limits (nothing accepted, every token -1). */
 ms_status ms_op_verify_draft(const float* target, int64_t ld_target, const float* draft, int64_t ld_draft,
                              const int32_t* tokens, const int32_t* row_start, int rows, int batch, int max_draft,
                              int vocab, const float* u_accept, const float* u_sample, int32_t* accepted,

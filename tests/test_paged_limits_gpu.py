@@ -124,3 +124,23 @@ def test_attention_where_the_heaviest_position_holds_nothing(kq, kkv, hd, T, nat
     # subtracted, so a probability is off by 2 * 3/2 U |s|; exp2 4 U above and below; the pairs 2^-21 or 2^-17; two sums of T
     tol = R.half_step(kq) * np.abs(ref) + A * (3 * U * spread + 8 * U + (2.0 ** -17 if kkv == "bf16" else 2.0 ** -21) + 2 * T * U)[..., None]
     assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / np.maximum(A, 1e-300)).max()
+
+
+# ---- verification ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("where", ["target", "draft"])
+@pytest.mark.parametrize("V", [50, 20000])
+def test_verification_flags_rows_with_nan(where, V):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(431)
+    target = torch.softmax(torch.randn((3, V), generator=g), 1).cuda()
+    draft = torch.softmax(torch.randn((1, V), generator=g), 1).cuda()
+    (target if where == "target" else draft)[0, 7] = float("nan")
+    tok = torch.tensor([3], dtype=torch.int32, device="cuda")
+    ua = torch.full((1,), 1 - 2.0 ** -24, device="cuda")
+    draft[0, 3] = 1.0                                                   # refused: u q >= p
+    acc, out = ms.verify_draft(target, draft, tok, R.starts([1, 0]).cuda(), 1, ua, torch.full((2,), 0.5, device="cuda"), status)
+    with pytest.raises(ms.MsError) as e:
+        ms.op_status(status)
+    assert e.value.status == ms.MS_ERR_TOKEN_RANGE
+    assert acc.cpu().tolist() == [0, 0] and out.cpu()[0].tolist() == [-1, -1] and out[1, 0].item() >= 0
