@@ -87,7 +87,8 @@ ms_status check_attn(const ms_paged_kv* kv, int q_elem, int n_heads, int max_row
     return bad(MS_ERR_SHAPE, who, "n_heads must be a multiple of n_kv_heads, at most 256 times it");
   if (max_rows < 1 || max_rows > 64) return bad(MS_ERR_SHAPE, who, "max_rows must be in [1, 64]");
   const long long tiles = (long long)kv->batch * n_heads * max_rows * (((long long)kv->max_pages * kv->page_size + 63) / 64);
-  if (tiles >= (1ll << 31)) return bad(MS_ERR_SHAPE, who, "batch * n_heads * max_rows * capacity is too large");
+  // the kernel counts in int, and adds a CTA's run to the count
+  if (tiles > (1ll << 30)) return bad(MS_ERR_SHAPE, who, "batch * n_heads * max_rows * capacity is too large");
   if ((long long)kv->n_kv_heads * ((n_heads / kv->n_kv_heads * max_rows + 15) / 16) >= (1ll << 31))
     return bad(MS_ERR_SHAPE, who, "too many heads");
   return MS_OK;

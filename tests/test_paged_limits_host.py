@@ -1,0 +1,13 @@
+"""Sizes that the paged-cache entry points refuse on the host.  No GPU needed."""
+from test_paged_host import SHAPE, attn, kv, ms
+
+L = ms._lib
+
+
+def test_attention_refuses_as_many_tiles_as_its_counts_could_not_pass():
+    # 993 sequences of 2162622 tiles of 64 positions are 2^31 - 2: the kernel rounds the count up to whole runs for its CTAs,
+    # which has to stay below 2^31 as well
+    huge = dict(max_pages=2162622, page_size=64, page_stride=1 << 12, batch=993, n_kv_heads=1)
+    assert 993 * 2162622 == 2 ** 31 - 2
+    assert attn(kv(**huge), heads=1, ldq=64, ldo=64, most=1, size=1 << 62) == SHAPE
+    assert L.ms_op_attn_paged_workspace(kv(**huge), ms.MS_ELEM_F16, 1, 1, 0) == 0
