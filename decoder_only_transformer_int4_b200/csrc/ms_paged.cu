@@ -23,6 +23,7 @@ bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 // every int32 or fp32 array among the arguments (null ones are checked apart)
 template <typename... Ptr>
 bool aligned4(Ptr... p) { return (aligned(p, 4) && ...); }
+constexpr int kMostRows = 1 << 30;   // row and block indices are ints, and some are rounded up
 size_t elem_bytes(int e) { return e == MS_ELEM_F32 ? 4 : 2; }
 
 // MS_OK, or the reason why the cache cannot be used.
@@ -89,8 +90,6 @@ ms_status check_attn(const ms_paged_kv* kv, int q_elem, int n_heads, int max_row
   const long long tiles = (long long)kv->batch * n_heads * max_rows * (((long long)kv->max_pages * kv->page_size + 63) / 64);
   // the kernel counts in int, and adds a CTA's run to the count
   if (tiles > (1ll << 30)) return bad(MS_ERR_SHAPE, who, "batch * n_heads * max_rows * capacity is too large");
-  if ((long long)kv->n_kv_heads * ((n_heads / kv->n_kv_heads * max_rows + 15) / 16) >= (1ll << 31))
-    return bad(MS_ERR_SHAPE, who, "too many heads");
   return MS_OK;
 }
 
@@ -130,7 +129,7 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
   const char* who = "ms_op_rope_append_paged";
   const ms_status s = check_kv(kv, who);
   if (s != MS_OK) return s;
-  if (rows < 0) return bad(MS_ERR_SHAPE, who, "rows < 0");
+  if (rows < 0 || rows > kMostRows) return bad(MS_ERR_SHAPE, who, "rows must be in [0, 2^30]");
   if (rows > 0 && (!k || !v)) return bad(MS_ERR_INVALID_ARG, who, "null pointer");
   if (!row_start || (rotary_dim > 0 && !inv_freq)) return bad(MS_ERR_INVALID_ARG, who, "null pointer");
   if (rows > 0 && !q != !q_out) return bad(MS_ERR_INVALID_ARG, who, "q and q_out go together");
@@ -171,7 +170,7 @@ ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, in
   const char* who = "ms_op_attn_paged";
   const ms_status s = check_attn(kv, q_elem, n_heads, max_rows, who);
   if (s != MS_OK) return s;
-  if (rows < 0) return bad(MS_ERR_SHAPE, who, "rows < 0");
+  if (rows < 0 || rows > kMostRows) return bad(MS_ERR_SHAPE, who, "rows must be in [0, 2^30]");
   if (!row_start || !workspace || (rows > 0 && (!q || !out))) return bad(MS_ERR_INVALID_ARG, who, "null pointer");
   if (!std::isfinite(scale)) return bad(MS_ERR_INVALID_ARG, who, "scale must be finite");
   const int64_t qw = (int64_t)n_heads * kv->head_dim, most = 1ll << 40;
@@ -216,7 +215,6 @@ ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t
   if (ldw < capacity || ldw_out < (keep < capacity ? keep : capacity) || ldw > (1ll << 40) || ldw_out > (1ll << 40))
     return bad(MS_ERR_SHAPE, who, "need ldw >= max_pages * page_size and ldw_out >= min(keep, max_pages * page_size)");
   if (weights_out == weights && ldw_out != ldw) return bad(MS_ERR_SHAPE, who, "in place, ldw_out must be ldw");
-  if (kv->n_kv_heads > 65535) return bad(MS_ERR_SHAPE, who, "too many heads");
   ms::EvictArgs a{view(*kv), weights, ldw, dst_table, dst_pages, keep, first, recent, kept, weights_out, ldw_out, lens_out};
   const ms::Launch L{static_cast<cudaStream_t>(stream), true, kv->status};
   return done(ms::launch_evict_paged(L, a), who);
@@ -228,8 +226,8 @@ ms_status ms_op_verify_draft(const float* target, int64_t ld_target, const float
                              uint32_t* status, void* stream) {
   const char* who = "ms_op_verify_draft";
   if (!target || !row_start || !u_sample || !accepted || !out) return bad(MS_ERR_INVALID_ARG, who, "null pointer");
-  if (rows < 0 || batch < 1 || batch > (1 << 20) || vocab < 1 || max_draft < 0 || max_draft > 256)
-    return bad(MS_ERR_SHAPE, who, "need rows >= 0, 1 <= batch <= 2^20, vocab >= 1 and 0 <= max_draft <= 256");
+  if (rows < 0 || rows > kMostRows || batch < 1 || batch > (1 << 20) || vocab < 1 || vocab > (1 << 30) || max_draft < 0 || max_draft > 256)
+    return bad(MS_ERR_SHAPE, who, "need rows <= 2^30, 1 <= batch <= 2^20, 1 <= vocab <= 2^30 and 0 <= max_draft <= 256");
   if (rows > 0 && max_draft > 0 && (!tokens || !u_accept)) return bad(MS_ERR_INVALID_ARG, who, "null pointer");
   if (!aligned4(target, draft, tokens, row_start, u_accept, u_sample, accepted, out, status))
     return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");

@@ -404,7 +404,7 @@ ms_status ms_op_status(uint32_t* status, void* stream);
  * the store.  Two rows of one call that name the same place of the same page (a page twice in the tables)
  * are written in no fixed order.
  * (q_elem, cache elem): (F32, F32), (F32, F16), (F16, F16), (BF16, BF16); else MS_ERR_UNSUPPORTED.
- * rotary_dim even, 0 .. head_dim, |position| < 2^30; n_heads >= 1. */
+ * rotary_dim even, 0 .. head_dim, |position| < 2^30; n_heads 1 .. 65536, rows <= 2^30. */
 ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, const void* k, int64_t ldk,
                                   const void* v, int64_t ldv, int q_elem, int rows, int n_heads,
                                   const int32_t* row_start, const int32_t* positions, const double* inv_freq,
@@ -430,7 +430,7 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
  * result of a sequence does not depend on timing, but its rounding on how the batch's work is split.
  * workspace: ms_op_attn_paged_workspace bytes (0 for arguments that the call refuses), 256-byte
  * aligned, holding nothing before or after; calls that may overlap on the GPU need their own, and their own weights.
- * max_pages * page_size < 2^30. */
+ * rows <= 2^30, max_pages * page_size < 2^30, batch * n_heads * max_rows * max_pages * page_size <= 2^36. */
 size_t ms_op_attn_paged_workspace(const ms_paged_kv* kv, int q_elem, int n_heads, int max_rows, int with_weights);
 ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, int q_elem, int rows, int max_rows,
                            int n_heads, float scale, const int32_t* row_start, void* out, int64_t ldo,
@@ -463,6 +463,7 @@ ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t
  * that is zero throughout), after n acceptances from p_n: the lowest v whose cumulative sum exceeds
  * u_sample[b] times the total.  Products and sums in double.
  * accepted int32 [batch]; out int32 [batch][max_draft + 1]: the accepted drafts, the next token, -1 behind.
+ * rows and vocab <= 2^30, batch <= 2^20.
  * Probabilities are finite and not negative (they need not sum to 1), random numbers in [0, 1).  A token outside
  * [0, vocab) is refused, weights to draw from (p_n, or what q_i leaves of p_i) that sum to nothing or not to a finite
  * number, or a u_sample outside [0, 1), give the next token -1; all flag status (may be NULL), as does a row range out of its limits (nothing accepted, every token -1). */

@@ -1,5 +1,5 @@
 """Sizes that the paged-cache entry points refuse on the host.  No GPU needed."""
-from test_paged_host import SHAPE, attn, kv, ms
+from test_paged_host import SHAPE, attn, kv, ms, rope, verify
 
 L = ms._lib
 
@@ -11,3 +11,12 @@ def test_attention_refuses_as_many_tiles_as_its_counts_could_not_pass():
     assert 993 * 2162622 == 2 ** 31 - 2
     assert attn(kv(**huge), heads=1, ldq=64, ldo=64, most=1, size=1 << 62) == SHAPE
     assert L.ms_op_attn_paged_workspace(kv(**huge), ms.MS_ELEM_F16, 1, 1, 0) == 0
+
+
+MOST = 1 << 30
+
+
+def test_rows_and_vocabularies_past_the_kernels_indices_are_refused():
+    for n in (MOST + 1, 2 ** 31 - 1):
+        assert rope(rows=n) == SHAPE and attn(rows=n) == SHAPE and verify(rows=n) == SHAPE
+        assert verify(vocab=n, ldt=1 << 32, ldd=1 << 32) == SHAPE
