@@ -141,6 +141,7 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
   const int64_t most = 1ll << 40;
   if (ldk < kw || ldv < kw || (q && (ldq < qw || ldq_out < qw)) || ldk > most || ldv > most || (q && (ldq > most || ldq_out > most)))
     return bad(MS_ERR_SHAPE, who, "a row stride is smaller than its row");
+  if (q && q_out == q && ldq_out != ldq && rows > 1) return bad(MS_ERR_SHAPE, who, "in place, ldq_out must be ldq");
   const size_t eb = elem_bytes(q_elem);
   if (!aligned(k, eb) || !aligned(v, eb) || !aligned(q, eb) || !aligned(q_out, eb) || !aligned(inv_freq, 8) || !aligned4(row_start, positions))
     return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
@@ -175,6 +176,7 @@ ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, in
   if (!std::isfinite(scale)) return bad(MS_ERR_INVALID_ARG, who, "scale must be finite");
   const int64_t qw = (int64_t)n_heads * kv->head_dim, most = 1ll << 40;
   if (ldq < qw || ldo < qw || ldq > most || ldo > most) return bad(MS_ERR_SHAPE, who, "a row stride is smaller than its row");
+  if (q && out == q && ldo != ldq && rows > 1) return bad(MS_ERR_SHAPE, who, "in place, ldo must be ldq");
   if (weights && (ldw < (int64_t)kv->max_pages * kv->page_size || ldw > most))
     return bad(MS_ERR_SHAPE, who, "ldw must hold max_pages * page_size positions");
   const size_t eb = elem_bytes(q_elem);

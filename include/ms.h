@@ -399,8 +399,8 @@ ms_status ms_op_status(uint32_t* status, void* stream);
  * then be NULL).  Scaled positions for long contexts are a matter of inv_freq and mscale; the angle
  * is reduced in double, so far positions keep their accuracy.  The position is the cache
  * index, or positions[r] (int32 [rows]) where not NULL: after an eviction the two differ.
- * q_out [rows][n_heads][head_dim] of q_elem at stride ldq_out, may be q itself; q may be NULL (then q_out
- * too): k and v alone.  k, v and q_out must not overlap the cache.  Turned in fp32, rounded once at
+ * q_out [rows][n_heads][head_dim] of q_elem at stride ldq_out, may be q itself (with ldq_out = ldq), else it
+ * must not overlap q, k or v; q may be NULL (then q_out too): k and v alone.  k, v and q_out must not overlap the cache.  Turned in fp32, rounded once at
  * the store.  Two rows of one call that name the same place of the same page (a page twice in the tables)
  * are written in no fixed order.
  * (q_elem, cache elem): (F32, F32), (F32, F16), (F16, F16), (BF16, BF16); else MS_ERR_UNSUPPORTED.
@@ -419,7 +419,8 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
  * A row that sees no position (T = 0, or n > T) gives 0.  What lies behind a sequence's end, or a row's last visible
  * position, never enters, whatever the memory holds; a k or v that is not finite makes the rows that see it so
  * (fp32: of magnitude below 2^127).  n <= max_rows (1 .. 64): one row is decoding,
- * several are drafts.  out may be q.  q and out [rows][n_heads][head_dim] of q_elem at strides ldq, ldo; rows behind
+ * several are drafts.  out may be q (with ldo = ldq), else they must not
+ * overlap.  q and out [rows][n_heads][head_dim] of q_elem at strides ldq, ldo; rows behind
  * row_start[batch] are left as they were.
  * weights (may be NULL): fp32 [batch][n_kv_heads][ldw], ldw >= max_pages * page_size: position t's entry
  * grows by the sum of p_t over the rows and the heads of its group (for ms_op_evict_paged).

@@ -1,5 +1,5 @@
 """Sizes that the paged-cache entry points refuse on the host.  No GPU needed."""
-from test_paged_host import SHAPE, attn, kv, ms, rope, verify
+from test_paged_host import P, SHAPE, attn, kv, ms, rope, verify
 
 L = ms._lib
 
@@ -20,3 +20,9 @@ def test_rows_and_vocabularies_past_the_kernels_indices_are_refused():
     for n in (MOST + 1, 2 ** 31 - 1):
         assert rope(rows=n) == SHAPE and attn(rows=n) == SHAPE and verify(rows=n) == SHAPE
         assert verify(vocab=n, ldt=1 << 32, ldd=1 << 32) == SHAPE
+
+
+def test_in_place_needs_the_same_row_stride():
+    # another stride would let one row's result overwrite another row's input
+    assert rope(out=P, ldo=1024) == SHAPE and "in place" in ms.last_error()
+    assert attn(out=P, ldo=1024) == SHAPE and "in place" in ms.last_error()
