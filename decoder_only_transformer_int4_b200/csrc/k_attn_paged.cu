@@ -48,6 +48,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
+#include <algorithm>
+#include <atomic>
 #include <type_traits>
 #include "ms_device.cuh"
 #include "ms_launch.cuh"
@@ -96,7 +98,7 @@ template <typename KT>
 constexpr float bias_of() { return std::is_same<KT, __half>::value ? 10.f : 0.f; }
 // fp32 results from a half cache: lo enters 2^12 times as large and its sum is scaled back.  The pair of a probability from
 // 2^-14 to 2^14 (the normal halves) is then off by 2^-22 of it: lo's step of 2^-24 counts 2^-36.  Smaller ones are brought
-// into that range before.  64 streams 19.8 us, 19.2 without; 32 sequences with 5 rows of 16 heads 41.8 us, 39.6 without.
+// into that range before.  64 streams 19.8 us, 19.2 without; 5% with several rows.
 constexpr float kLoUp = 4096.f, kPairFrom = 0x1p-14f;
 // How far a score may pass the running reference before sums are scaled anew: probabilities stay below 2^14
 constexpr float kSlack = 4.f;
@@ -1299,6 +1301,11 @@ auto with_nb(int nb, F&& f) {
   return nb == 2 ? f(std::integral_constant<int, 2>()) : f(std::integral_constant<int, 1>());
 }
 
+// CTAs of a kernel that the registers of an SM hold, set with its attributes before the first plan (one architecture, so the
+// same on every device).
+template <typename KT, bool Q32, int HD, int NB>
+std::atomic<int> g_reg_ctas{0};
+
 // Sizes of one call, the same for the workspace and for the launch.
 struct Plan {
   int nb, R, hpg, rb, grid, cluster;
@@ -1316,7 +1323,10 @@ Plan plan_for(const AttnPagedArgs& a, int n_sm) {
   p.nb = (int)((rows + p.rb * 8 - 1) / (p.rb * 8));
   p.R = 8 * p.nb;
   p.smem = with_nb<KT>(p.nb, [&](auto nb) { return Shape<KT, Q32, HD, decltype(nb)::value>::smem(a.c.batch); });
-  const int fit = (int)((228 * 1024) / (p.smem + 1024));
+  // CTAs an SM: what shared memory and registers leave (28 rows of 64 elements take 254 registers, so that two fit where
+  // shared memory would allow three: 45.4 us for 32 sequences of 7 rows and 16 heads, 52.6 planned with three), three at most
+  const int regs = with_nb<KT>(p.nb, [](auto nb) { return g_reg_ctas<KT, Q32, HD, decltype(nb)::value>.load(std::memory_order_relaxed); });
+  const int fit = std::min((int)((228 * 1024) / (p.smem + 1024)), regs);
   const int per_sm = fit < 1 ? 1 : fit > 3 ? 3 : fit;
   const long long tiles = (long long)a.c.batch * a.c.Hk * p.rb * ((a.c.capacity() + kTile - 1) / kTile);
   const long long resident = (long long)per_sm * n_sm;
@@ -1406,6 +1416,10 @@ struct DoAttrs {
     for (int i = 1; i <= kMostTiles<KT> && e == cudaSuccess; ++i)
       e = with_nb<KT>(i, [&](auto nb) {
         constexpr int NB = decltype(nb)::value;
+        int ctas = 0;
+        const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, attn_paged_kernel<KT, Q32, HD, NB>, kThreads, 0);
+        if (err != cudaSuccess) return err;
+        g_reg_ctas<KT, Q32, HD, NB>.store(ctas, std::memory_order_relaxed);
         return allow_smem(attn_paged_kernel<KT, Q32, HD, NB>, Shape<KT, Q32, HD, NB>::smem(kPagedMaxBatch));
       });
     return e;

@@ -144,3 +144,18 @@ def test_verification_flags_rows_with_nan(where, V):
         ms.op_status(status)
     assert e.value.status == ms.MS_ERR_TOKEN_RANGE
     assert acc.cpu().tolist() == [0, 0] and out.cpu()[0].tolist() == [-1, -1] and out[1, 0].item() >= 0
+
+
+# ---- how the attention's work is laid out -------------------------------------------------------------
+
+@pytest.mark.parametrize("kq,kkv,group", [("f16", "f16", 28), ("bf16", "bf16", 32), ("f32", "f16", 25), ("f32", "f16", 24)])
+def test_attention_plans_no_more_ctas_than_fit(kq, kkv, group):
+    """The workspace holds two slots of (hd + 2) floats a row for each CTA of the grid.  Three CTAs of 128 threads an SM leave 168
+    registers a thread; the kernels of these shapes (24 and more rows of 64 elements in registers) need more, so two fit."""
+    hd, page, batch = 64, 256, 64
+    table = torch.zeros((batch, 64), dtype=torch.int32, device="cuda")
+    k = torch.zeros((1, 1, page, hd), dtype=R.TYPES[kkv], device="cuda")
+    kv = ms.PagedKV(k, k.clone(), table, torch.zeros(batch, dtype=torch.int32, device="cuda"))
+    rows = -(-group // 8) * 8
+    ctas = ms.attn_paged_workspace(kv, R.TYPES[kq], group, 1) / (2 * rows * (hd + 2) * 4)
+    assert round(ctas) == 2 * torch.cuda.get_device_properties(0).multi_processor_count
