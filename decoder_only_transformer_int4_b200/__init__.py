@@ -12,6 +12,7 @@ back to.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import re
 from typing import List, Optional, Sequence, Tuple
@@ -26,7 +27,25 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "ms.h")
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python decoder_only_transformer_int4_b200/build.py`")
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _paged  # noqa: E402  (the paged operators' calls; refers to the library just loaded)
+
+
+class _MissingExtension:
+    """Stands for the extension module where it does not load (it belongs to one Python and one torch): what goes
+    through ctypes works without it, a call of the paged operators says what is missing."""
+
+    def __init__(self, why: str):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the paged operators' extension module does not load ({self.why}): build it for this Python and "
+                          "torch with `python decoder_only_transformer_int4_b200/build.py`")
+
+
+try:
+    # the paged operators' calls; refers to the library just loaded
+    _paged = importlib.import_module(__name__ + "._paged")
+except ImportError as _e:
+    _paged = _MissingExtension(str(_e))
 
 MS_OK, MS_ERR_INVALID_ARG, MS_ERR_SHAPE, MS_ERR_CACHE_FULL, MS_ERR_TOKEN_RANGE = 0, 1, 2, 3, 4
 MS_ERR_OOM, MS_ERR_CUDA, MS_ERR_TIMEOUT, MS_ERR_UNSUPPORTED = 5, 6, 7, 8

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -23,6 +24,7 @@ SOURCES = ["k_elementwise.cu", "k_gemv.cu", "k_gemm_f16.cu", "k_w4a8.cu", "k_gem
            "ms_noalloc.cu", "k_paged.cu", "k_attn_paged.cu", "k_verify.cu", "ms_paged.cu"]
 EXT = os.path.join(HERE, "_paged" + sysconfig.get_config_var("EXT_SUFFIX"))
 EXT_SOURCE = "py_paged.cpp"
+EXT_STAMP = os.path.join(BUILD, "extension")   # what it was built for
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]
@@ -59,6 +61,18 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _extension_for() -> str:
+    """The torch and the Python that the extension is built for."""
+    return f"torch {importlib.metadata.version('torch')}, Python {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def _extension_stale() -> bool:
+    if _stale(EXT, EXT_SOURCE) or not os.path.exists(EXT_STAMP):
+        return True
+    with open(EXT_STAMP) as f:
+        return f.read() != _extension_for()
+
+
 def _build_extension() -> None:
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -73,6 +87,8 @@ def _build_extension() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"{EXT_SOURCE} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
+    with open(EXT_STAMP, "w") as f:
+        f.write(_extension_for())
 
 
 def build(force: bool = False, ptxas_v: bool = False) -> str:
@@ -89,7 +105,7 @@ def build(force: bool = False, ptxas_v: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    if force or _stale(EXT, EXT_SOURCE):
+    if force or _extension_stale():
         _build_extension()
     return LIB
 
