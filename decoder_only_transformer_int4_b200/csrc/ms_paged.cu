@@ -104,6 +104,21 @@ ms::AttnPagedArgs attn_args(const ms_paged_kv& kv, int n_heads, int max_rows, fl
 
 }  // namespace
 
+namespace ms {
+
+ms_status check_evict_sizes(const ms_paged_kv& kv, int64_t ldw, int dst_pages, int keep, int first, int recent, int64_t ldw_out) {
+  const char* who = "ms_op_evict_paged";
+  if (keep < 1 || first < 0 || recent < 0 || (int64_t)first + recent > keep)
+    return bad(MS_ERR_SHAPE, who, "need keep >= 1, first, recent >= 0 and first + recent <= keep");
+  const int64_t capacity = (int64_t)kv.max_pages * kv.page_size;
+  if (dst_pages < 1) return bad(MS_ERR_SHAPE, who, "need dst_pages >= 1");
+  if (ldw < capacity || ldw_out < (keep < capacity ? keep : capacity) || ldw > (1ll << 40) || ldw_out > (1ll << 40))
+    return bad(MS_ERR_SHAPE, who, "need ldw >= max_pages * page_size and ldw_out >= min(keep, max_pages * page_size)");
+  return MS_OK;
+}
+
+}  // namespace ms
+
 extern "C" {
 
 ms_status ms_op_status(uint32_t* status, void* stream) {
@@ -210,12 +225,8 @@ ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t
   if (!weights || !dst_table || !kept || !weights_out || !lens_out) return bad(MS_ERR_INVALID_ARG, who, "null pointer");
   if (!aligned4(weights, dst_table, kept, weights_out, lens_out)) return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
   if (lens_out == kv->lens) return bad(MS_ERR_INVALID_ARG, who, "lens_out must not be the cache's lens");
-  if (keep < 1 || first < 0 || recent < 0 || (int64_t)first + recent > keep)
-    return bad(MS_ERR_SHAPE, who, "need keep >= 1, first, recent >= 0 and first + recent <= keep");
-  const int64_t capacity = (int64_t)kv->max_pages * kv->page_size;
-  if (dst_pages < 1) return bad(MS_ERR_SHAPE, who, "need dst_pages >= 1");
-  if (ldw < capacity || ldw_out < (keep < capacity ? keep : capacity) || ldw > (1ll << 40) || ldw_out > (1ll << 40))
-    return bad(MS_ERR_SHAPE, who, "need ldw >= max_pages * page_size and ldw_out >= min(keep, max_pages * page_size)");
+  const ms_status sizes = ms::check_evict_sizes(*kv, ldw, dst_pages, keep, first, recent, ldw_out);
+  if (sizes != MS_OK) return sizes;
   if (weights_out == weights && ldw_out != ldw) return bad(MS_ERR_SHAPE, who, "in place, ldw_out must be ldw");
   ms::EvictArgs a{view(*kv), weights, ldw, dst_table, dst_pages, keep, first, recent, kept, weights_out, ldw_out, lens_out};
   const ms::Launch L{static_cast<cudaStream_t>(stream), true, kv->status};

@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include "../../include/ms.h"
 #include "ms_kernels.h"
 
 namespace ms {
@@ -68,6 +69,8 @@ struct EvictArgs {
   int* lens_out;           // [batch]
 };
 cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a);
+// What ms_op_evict_paged says to these sizes; for callers that allocate the outputs.
+ms_status check_evict_sizes(const ms_paged_kv& kv, int64_t ldw, int dst_pages, int keep, int first, int recent, int64_t ldw_out);
 
 struct VerifyArgs {
   const float* target;     // rows at stride ldt

@@ -20,6 +20,7 @@
 #include <string>
 
 #include "../../include/ms.h"
+#include "ms_paged.h"
 
 namespace {
 
@@ -243,21 +244,27 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     weights = static_cast<float*>(flat(w, "weights", at::kFloat, {kv.s.batch, kv.s.n_kv_heads, ldw}, kv.dev));
   }
   const c10::OptionalDeviceGuard on(kv.dev);
-  const at::Tensor out = none(a[6]) ? at::empty({rows, heads, hd}, q.options()) : tensor(a[6], "out");
-  const Rows orow = packed_rows(out, "out", heads, hd, type, kv.dev);
-  if (out.size(0) != rows) refuse("q and out", "expected the same number of rows");
-  at::Tensor ws;
-  if (none(a[7])) {
-    const size_t bytes = ms_op_attn_paged_workspace(&kv.s, q_elem, as_int(heads, "q"), max_rows, weights != nullptr);
-    ws = at::empty({(int64_t)std::max<size_t>(bytes, 1)}, q.options().dtype(at::kByte));
-  } else {
+  // 0 for sizes that the call refuses: nothing is allocated for them
+  const size_t bytes = ms_op_attn_paged_workspace(&kv.s, q_elem, as_int(heads, "q"), max_rows, weights != nullptr);
+  at::Tensor out, ws;
+  if (!none(a[6])) out = tensor(a[6], "out");
+  else if (bytes) out = at::empty({rows, heads, hd}, q.options());
+  Rows orow;
+  if (out.defined()) {
+    orow = packed_rows(out, "out", heads, hd, type, kv.dev);
+    if (out.size(0) != rows) refuse("q and out", "expected the same number of rows");
+  }
+  if (!none(a[7])) {
     ws = tensor(a[7], "workspace");
     if (ws.scalar_type() != at::kByte || ws.device() != kv.dev || !ws.is_contiguous()) refuse("workspace", "expected contiguous uint8 on " + kv.dev.str());
+  } else if (bytes) {
+    ws = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
   }
   const ms_status s = ms_op_attn_paged(&kv.s, qr.p, qr.ld, q_elem, as_int(rows, "q"), max_rows, as_int(heads, "q"), scale,
-                                       static_cast<const int32_t*>(start), orow.p, orow.ld, weights, ldw, ws.data_ptr(), ws.numel(),
+                                       static_cast<const int32_t*>(start), orow.p, orow.ld, weights, ldw, ws.defined() ? ws.data_ptr() : nullptr,
+                                       ws.defined() ? ws.numel() : 0,
                                        current_stream(kv.dev));
-  return give(s, &out);
+  return out.defined() ? give(s, &out) : give(s);
   END_HANDLE_TH_ERRORS
 }
 
@@ -275,10 +282,15 @@ PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* dp = flat(dst, "dst_table", at::kInt, {batch, pages}, kv.dev);
   const int keep = int_arg(a[3], "keep"), first = int_arg(a[4], "first"), recent = int_arg(a[5], "recent");
   const c10::OptionalDeviceGuard on(kv.dev);
-  const at::Tensor wo = none(a[6]) ? at::empty_like(w) : tensor(a[6], "weights_out");
-  const int64_t ldwo = wo.dim() == 3 ? wo.size(2) : 0;
-  float* wop = static_cast<float*>(flat(wo, "weights_out", at::kFloat, {batch, hk, ldwo}, kv.dev));
-  const at::Tensor kept = at::empty({batch, hk, std::max(keep, 0)}, dst.options()), lens = at::empty({batch}, dst.options());
+  // refused sizes are found before anything is allocated for them
+  const at::Tensor* given = none(a[6]) ? nullptr : &tensor(a[6], "weights_out");
+  const int64_t ldwo = !given ? ldw : given->dim() == 3 ? given->size(2) : 0;
+  if (given) flat(*given, "weights_out", at::kFloat, {batch, hk, ldwo}, kv.dev);
+  const ms_status refused = ms::check_evict_sizes(kv.s, ldw, as_int(pages, "dst_table"), keep, first, recent, ldwo);
+  if (refused != MS_OK) return give(refused);
+  const at::Tensor wo = given ? *given : at::empty_like(w);
+  float* wop = static_cast<float*>(wo.data_ptr());
+  const at::Tensor kept = at::empty({batch, hk, keep}, dst.options()), lens = at::empty({batch}, dst.options());
   const ms_status s = ms_op_evict_paged(&kv.s, wp, ldw, static_cast<const int32_t*>(dp), as_int(pages, "dst_table"), keep, first, recent,
                                         static_cast<int32_t*>(kept.data_ptr()), wop, ldwo, static_cast<int32_t*>(lens.data_ptr()),
                                         current_stream(kv.dev));

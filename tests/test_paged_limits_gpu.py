@@ -159,3 +159,24 @@ def test_attention_plans_no_more_ctas_than_fit(kq, kkv, group):
     rows = -(-group // 8) * 8
     ctas = ms.attn_paged_workspace(kv, R.TYPES[kq], group, 1) / (2 * rows * (hd + 2) * 4)
     assert round(ctas) == 2 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+# ---- torch's side of a call ---------------------------------------------------------------------------
+
+def test_refused_calls_allocate_nothing():
+    pages = R.Pages([40, 3], 2, 16, 64, "f16", seed=441, spare=6)
+    kv = pages.cuda(ms)
+    w = torch.zeros((2, 2, kv.capacity), device="cuda")
+    dst = torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    q, st = torch.zeros((2, 6, 64), dtype=torch.float16, device="cuda"), R.starts([1, 1]).cuda()
+    for call, code in ((lambda: ms.evict_paged(kv, w, dst, 1 << 20, first=(1 << 20) + 1), ms.MS_ERR_SHAPE),
+                       (lambda: ms.evict_paged(kv, w[..., :16].contiguous(), dst, 1 << 20), ms.MS_ERR_SHAPE),
+                       (lambda: ms.attn_paged(kv, q.expand(2, 6, 64).bfloat16().repeat(1 << 10, 1, 1), st, 1), ms.MS_ERR_UNSUPPORTED),
+                       (lambda: ms.attn_paged(kv, q[:, :5].repeat(1 << 10, 1, 1), st, 1), ms.MS_ERR_SHAPE)):
+        torch.cuda.synchronize()
+        n0 = torch.cuda.memory_stats()["allocation.all.allocated"]
+        with pytest.raises(ms.MsError) as e:
+            call()
+        assert e.value.status == code
+        made = torch.cuda.memory_stats()["allocation.all.allocated"] - n0
+        assert made <= 2, made                                          # the arguments of the call alone
