@@ -313,7 +313,8 @@ class PagedKV:
     """One layer's paged cache (ms_paged_kv): K and V pages [n_pages, kv_heads, page_size, head_dim] (the
     first dimension may be strided), table int32 [batch, max_pages], lens int32 [batch] with the rows of
     the next call included; status (optional): int32 [1], zeroed, collects errors in device data (op_status).
-    Holds the tensors; writes to them in place are seen by later calls."""
+    Holds the tensors; writes to them in place are seen by later calls.  The operators serve: they are no part of a
+    gradient's graph (results are detached from inputs that require one), and what they write in place counts as written."""
 
     __slots__ = ("_h", "_sizes", "_tensors")
 

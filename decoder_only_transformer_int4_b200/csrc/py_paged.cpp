@@ -94,6 +94,12 @@ float float_arg(PyObject* o) {
   return static_cast<float>(v);
 }
 
+// A call writes into the tensor: autograd sees a new version of it, so that a backward pass which needs the old values
+// is refused by torch instead of reading the new ones.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The cache's description, its device and the tensors that it points into.
 struct Kv {
   ms_paged_kv s;
@@ -206,6 +212,11 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                               static_cast<const int32_t*>(start), static_cast<const int32_t*>(pos),
                                               static_cast<const double*>(freq), as_int(2 * pairs, "inv_freq"), turn, mscale, orow.p, orow.ld,
                                               current_stream(kv.dev));
+  if (s == MS_OK) {
+    written(kv.held[0]);
+    written(kv.held[1]);
+    if (!none(a[9])) written(out);
+  }
   return out.defined() ? give(s, &out) : give(s);
   END_HANDLE_TH_ERRORS
 }
@@ -264,6 +275,10 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                        static_cast<const int32_t*>(start), orow.p, orow.ld, weights, ldw, ws.defined() ? ws.data_ptr() : nullptr,
                                        ws.defined() ? ws.numel() : 0,
                                        current_stream(kv.dev));
+  if (s == MS_OK) {
+    if (weights) written(THPVariable_Unpack(a[5]));
+    if (!none(a[6])) written(out);
+  }
   return out.defined() ? give(s, &out) : give(s);
   END_HANDLE_TH_ERRORS
 }
@@ -294,6 +309,11 @@ PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const ms_status s = ms_op_evict_paged(&kv.s, wp, ldw, static_cast<const int32_t*>(dp), as_int(pages, "dst_table"), keep, first, recent,
                                         static_cast<int32_t*>(kept.data_ptr()), wop, ldwo, static_cast<int32_t*>(lens.data_ptr()),
                                         current_stream(kv.dev));
+  if (s == MS_OK) {
+    written(kv.held[0]);
+    written(kv.held[1]);
+    if (given) written(wo);
+  }
   return give(s, &kept, &wo, &lens);
   END_HANDLE_TH_ERRORS
 }

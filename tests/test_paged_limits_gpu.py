@@ -180,3 +180,28 @@ def test_refused_calls_allocate_nothing():
         assert e.value.status == code
         made = torch.cuda.memory_stats()["allocation.all.allocated"] - n0
         assert made <= 2, made                                          # the arguments of the call alone
+
+
+def test_calls_count_as_writes():
+    """Pages, weights and outputs that a call writes carry a new version, so that autograd notices."""
+    pages = R.Pages([40], 1, 16, 64, "f32", seed=451, spare=8)
+    kv = pages.cuda(ms)
+    x, st = torch.randn((1, 1, 64), device="cuda"), R.starts([1]).cuda()
+    w, out = torch.zeros((1, 1, kv.capacity), device="cuda"), torch.empty((1, 1, 64), device="cuda")
+    dst = torch.tensor([pages.free[:1]], dtype=torch.int32, device="cuda")
+
+    def versions():
+        return [t._version for t in (pages.dk, pages.dv, w, out)]
+
+    for call, written in ((lambda: ms.rope_append_paged(kv, x, x, x, st, None, out=out), (1, 1, 0, 1)),
+                          (lambda: ms.rope_append_paged(kv, None, x, x, st, None), (1, 1, 0, 0)),
+                          (lambda: ms.attn_paged(kv, x, st, 1, weights=w, out=out), (0, 0, 1, 1)),
+                          (lambda: ms.attn_paged(kv, x, st, 1), (0, 0, 0, 0)),
+                          (lambda: ms.evict_paged(kv, w, dst, 16), (1, 1, 0, 0)),
+                          (lambda: ms.evict_paged(kv, w, dst, 16, weights_out=w), (1, 1, 1, 0))):
+        before = versions()
+        call()
+        assert tuple(b > a for a, b in zip(before, versions())) == tuple(map(bool, written))
+    with torch.inference_mode():                                        # such tensors have no version
+        w2 = torch.zeros((1, 1, kv.capacity), device="cuda")
+        ms.attn_paged(kv, x, st, 1, weights=w2)
