@@ -139,11 +139,14 @@ PyObject* py_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &table = tensor(a[2], "table"), &lens = tensor(a[3], "lens");
   const at::Device dev = k.device();
   if (!dev.is_cuda()) refuse("k", "expected CUDA tensors");
-  if (k.dim() != 4 || k.sizes() != v.sizes() || k.strides() != v.strides() || k.scalar_type() != v.scalar_type() || v.device() != dev)
+  if (k.dim() != 4 || k.sizes() != v.sizes() || k.scalar_type() != v.scalar_type() || v.device() != dev)
     refuse("k and v", "expected the same pages [n_pages, kv_heads, page_size, head_dim]");
   const int64_t np = k.size(0), hk = k.size(1), page = k.size(2), hd = k.size(3);
-  if (k.stride(3) != 1 || (k.stride(2) != hd && page > 1) || (k.stride(1) != page * hd && hk > 1))
-    refuse("k and v", "the elements of a page must lie together");
+  // the stride of a dimension of one means nothing
+  if (np > 1 && k.stride(0) != v.stride(0)) refuse("k and v", "expected the same stride from page to page");
+  for (const at::Tensor* t : {&k, &v})
+    if ((t->stride(3) != 1 && hd > 1) || (t->stride(2) != hd && page > 1) || (t->stride(1) != page * hd && hk > 1))
+      refuse("k and v", "the elements of a page must lie together");
   if (table.dim() != 2) refuse("table", "expected [batch, max_pages]");
   const int64_t batch = table.size(0), most = table.size(1);
   std::unique_ptr<Kv> kv(new Kv{{}, dev, {k, v, table, lens}});

@@ -1,4 +1,5 @@
-"""The paged-cache operators at the edges of what they take."""
+"""The paged-cache operators at the edges of what they take: row ranges and lengths out of their limits, values at the ends
+of their types' ranges, handles of odd strides, what a call does to torch's own state."""
 import numpy as np
 import pytest
 import torch
@@ -205,3 +206,16 @@ def test_calls_count_as_writes():
     with torch.inference_mode():                                        # such tensors have no version
         w2 = torch.zeros((1, 1, kv.capacity), device="cuda")
         ms.attn_paged(kv, x, st, 1, weights=w2)
+
+
+def test_a_cache_of_one_page_may_have_any_stride_there():
+    big = torch.randn((2, 1, 16, 64), device="cuda")
+    k, v = big[:1].as_strided((1, 1, 16, 64), (5000, 77, 64, 1)), big[1:]
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.full((1,), 16, dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 1, 64), device="cuda")
+    got = ms.attn_paged(ms.PagedKV(k, v, table, lens), q, R.starts([1]).cuda(), 1)
+    want = ms.attn_paged(ms.PagedKV(big[:1], v, table, lens), q, R.starts([1]).cuda(), 1)
+    assert torch.equal(got, want)
+    for bad in (big[1:].expand(1, 1, 16, 64).transpose(2, 3), big.half()[1:], big):
+        with pytest.raises(ValueError):
+            ms.PagedKV(k, bad, table, lens)
