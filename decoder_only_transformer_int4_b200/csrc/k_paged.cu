@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_paged_kernel(Rope
 }
 
 template <typename QT, typename KT>
-static cudaError_t rope_go(const Launch& L, const RopeArgs& a) {
+static cudaError_t rope_go(const Launch& L, const RopeArgs& a, int n_sm) {
   constexpr int VEC = 16 / sizeof(QT);
   auto off = [&](const void* p, long long ld) { return p && ((reinterpret_cast<uintptr_t>(p) & 15) || ld % VEC != 0); };
   // 16-byte accesses need aligned rows, and half-layout pairs that fall on whole chunks
@@ -330,23 +330,23 @@ static cudaError_t rope_go(const Launch& L, const RopeArgs& a) {
   // 8, 103 at 4, 105 at 16).
   int tokens = 1;
   const int items = ((a.q ? a.H : 0) + 2 * a.c.Hk) * a.c.hd / (vector ? 2 * VEC : 2), most = std::min(kRopeTokens, kRopeThreads * 2 * VEC / a.c.hd);
-  while (tokens < most && a.rows >= 148 * 2 * 2 * tokens && (tokens * items < 2 * kRopeThreads || (tokens < 8 && a.rows >= 148 * 6 * 2 * tokens))) tokens *= 2;
+  while (tokens < most && a.rows >= (long long)n_sm * 2 * 2 * tokens && (tokens * items < 2 * kRopeThreads || (tokens < 8 && a.rows >= (long long)n_sm * 6 * 2 * tokens))) tokens *= 2;
   // or as many as make one wave of all blocks, each with 24 items a thread at most (3000 rows of 72 heads: 10% faster at 8
   // than at 2)
   int wave = 1;
-  while (wave < most && a.rows > (long long)148 * 4 * wave) wave *= 2;
-  if (a.rows <= (long long)148 * 4 * wave && wave * items <= 24 * kRopeThreads) tokens = std::max(tokens, wave);
+  while (wave < most && a.rows > (long long)n_sm * 4 * wave) wave *= 2;
+  if (a.rows <= (long long)n_sm * 4 * wave && wave * items <= 24 * kRopeThreads) tokens = std::max(tokens, wave);
   const dim3 grid((a.rows + tokens - 1) / tokens), block(kRopeThreads);
   if (vector) return launch_k(L, rope_append_paged_kernel<QT, KT, true>, grid, block, 0, a, tokens);
   return launch_k(L, rope_append_paged_kernel<QT, KT, false>, grid, block, 0, a, tokens);
 }
 
-cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_elem) {
+cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_elem, int n_sm) {
   if (a.rows <= 0) return cudaSuccess;
-  if (q_elem == kF32 && a.c.elem == kF32) return rope_go<float, float>(L, a);
-  if (q_elem == kF32 && a.c.elem == kElemF16) return rope_go<float, __half>(L, a);
-  if (q_elem == kElemF16 && a.c.elem == kElemF16) return rope_go<__half, __half>(L, a);
-  if (q_elem == kBf16 && a.c.elem == kBf16) return rope_go<__nv_bfloat16, __nv_bfloat16>(L, a);
+  if (q_elem == kF32 && a.c.elem == kF32) return rope_go<float, float>(L, a, n_sm);
+  if (q_elem == kF32 && a.c.elem == kElemF16) return rope_go<float, __half>(L, a, n_sm);
+  if (q_elem == kElemF16 && a.c.elem == kElemF16) return rope_go<__half, __half>(L, a, n_sm);
+  if (q_elem == kBf16 && a.c.elem == kBf16) return rope_go<__nv_bfloat16, __nv_bfloat16>(L, a, n_sm);
   return cudaErrorInvalidValue;
 }
 
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_rows_kernel(EvictArgs a, 
   move_rows(a, row_shift, blockIdx.z, blockIdx.y, a.lens_out[blockIdx.z], blockIdx.x, gridDim.x);
 }
 
-cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a) {
+cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a, int n_sm) {
   const int chunks = a.c.hd * (a.c.elem == kF32 ? 4 : 2) / 16;   // 8, 16 or 32
   const int shift = chunks == 8 ? 3 : chunks == 16 ? 4 : 5;
   const long long units = (long long)a.c.Hk * a.c.batch;
@@ -655,14 +655,14 @@ cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a) {
   // cluster's barriers (52 units of 170 rows of 256 bytes: 9.6 us alone, 13.8 in fours).
   const long long bytes = (long long)std::min(a.keep, a.c.capacity()) * chunks * 16 * 2;
   int C = 1;
-  while (C < kEvMaxCluster && units * C * 2 <= 2 * 148 && (bytes > C * (128ll << 10) || a.c.capacity() > C * 2 * kEvThreads)) C *= 2;
+  while (C < kEvMaxCluster && units * C * 2 <= 2 * n_sm && (bytes > C * (128ll << 10) || a.c.capacity() > C * 2 * kEvThreads)) C *= 2;
   // Fewer CTAs than SMs with much to move: the rows get a grid of their own (4 units of 14191 fp32 rows of 128: 37 us,
   // 93 where the clusters move them).
-  const bool apart = units * C < 148 && bytes > C * (256ll << 10);
+  const bool apart = units * C < n_sm && bytes > C * (256ll << 10);
   const cudaError_t e = launch_cluster(L, evict_paged_kernel, C, dim3((unsigned)(units * C)), dim3(kEvThreads), 0, a, shift, apart ? 0 : 1);
   if (e != cudaSuccess || !apart) return e;
   const int at_once = (kEvThreads >> shift) * 4;
-  const int blocks = std::min<long long>((std::min(a.keep, a.c.capacity()) + at_once - 1) / at_once, 4 * 148 / units + 1);
+  const int blocks = std::min<long long>((std::min(a.keep, a.c.capacity()) + at_once - 1) / at_once, 4 * n_sm / units + 1);
   return launch_k(L, evict_rows_kernel, dim3(blocks, a.c.Hk, a.c.batch), dim3(kEvThreads), 0, a, shift);
 }
 

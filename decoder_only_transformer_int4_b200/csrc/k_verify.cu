@@ -211,11 +211,11 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_draft_kernel(VerifyArgs
   if (lane == 0) out[taken] = lo;
 }
 
-cudaError_t launch_verify_draft(const Launch& L, const VerifyArgs& a) {
+cudaError_t launch_verify_draft(const Launch& L, const VerifyArgs& a, int n_sm) {
   // a CTA for each 8192 tokens of the row (16 a thread: one or two rounds of loads), up to a portable cluster and to two an
   // SM in all (43 sequences of 72091: 13.1 us in clusters of 4, 15.2 in more than fit at once)
   int C = 1;
-  while (C < kVerMaxCluster && C * 8192 < a.V && (long long)a.batch * C * 2 <= 2 * 148) C *= 2;
+  while (C < kVerMaxCluster && C * 8192 < a.V && (long long)a.batch * C * 2 <= 2 * n_sm) C *= 2;
   return launch_cluster(L, verify_draft_kernel, C, dim3(a.batch * C), dim3(kVerThreads), 0, a, L.status);
 }
 

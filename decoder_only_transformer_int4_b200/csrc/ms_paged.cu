@@ -161,10 +161,13 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
   if (!aligned(k, eb) || !aligned(v, eb) || !aligned(q, eb) || !aligned(q_out, eb) || !aligned(inv_freq, 8) || !aligned4(row_start, positions))
     return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
   if (rows == 0) return MS_OK;
+  int n_sm = 0;
+  const cudaError_t e = ready(&n_sm);
+  if (e != cudaSuccess) return done(e, who);
   ms::RopeArgs a{view(*kv), q,       k,          v,         ldq,                 ldk,    ldv,      ldq_out,   q_out,
                  rows,      q ? n_heads : 0, rotary_dim, interleaved ? 1 : 0, mscale, inv_freq, row_start, positions};
   const ms::Launch L{static_cast<cudaStream_t>(stream), true, kv->status};
-  return done(ms::launch_rope_append_paged(L, a, q_elem), who);
+  return done(ms::launch_rope_append_paged(L, a, q_elem, n_sm), who);
 }
 
 size_t ms_op_attn_paged_workspace(const ms_paged_kv* kv, int q_elem, int n_heads, int max_rows, int with_weights) {
@@ -228,9 +231,12 @@ ms_status ms_op_evict_paged(const ms_paged_kv* kv, const float* weights, int64_t
   const ms_status sizes = ms::check_evict_sizes(*kv, ldw, dst_pages, keep, first, recent, ldw_out);
   if (sizes != MS_OK) return sizes;
   if (weights_out == weights && ldw_out != ldw) return bad(MS_ERR_SHAPE, who, "in place, ldw_out must be ldw");
+  int n_sm = 0;
+  const cudaError_t e = ready(&n_sm);
+  if (e != cudaSuccess) return done(e, who);
   ms::EvictArgs a{view(*kv), weights, ldw, dst_table, dst_pages, keep, first, recent, kept, weights_out, ldw_out, lens_out};
   const ms::Launch L{static_cast<cudaStream_t>(stream), true, kv->status};
-  return done(ms::launch_evict_paged(L, a), who);
+  return done(ms::launch_evict_paged(L, a, n_sm), who);
 }
 
 ms_status ms_op_verify_draft(const float* target, int64_t ld_target, const float* draft, int64_t ld_draft,
@@ -246,9 +252,12 @@ ms_status ms_op_verify_draft(const float* target, int64_t ld_target, const float
     return bad(MS_ERR_INVALID_ARG, who, "a pointer is not aligned to its elements");
   if (ld_target < vocab || (draft && ld_draft < vocab) || ld_target > (1ll << 40) || ld_draft > (1ll << 40))
     return bad(MS_ERR_SHAPE, who, "a row stride is smaller than the vocabulary");
+  int n_sm = 0;
+  const cudaError_t e = ready(&n_sm);
+  if (e != cudaSuccess) return done(e, who);
   ms::VerifyArgs a{target, draft, ld_target, ld_draft, tokens, row_start, rows, batch, max_draft, vocab, u_accept, u_sample, accepted, out};
   const ms::Launch L{static_cast<cudaStream_t>(stream), true, status};
-  return done(ms::launch_verify_draft(L, a), who);
+  return done(ms::launch_verify_draft(L, a, n_sm), who);
 }
 
 }  // extern "C"

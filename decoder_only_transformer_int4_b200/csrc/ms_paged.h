@@ -39,7 +39,8 @@ struct RopeArgs {
   const int* row_start;    // [batch + 1]
   const int* positions;    // [rows] or null
 };
-cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_elem);
+// (n_sm: the device's SMs, by which all of these lay out their grids)
+cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_elem, int n_sm);
 
 struct AttnPagedArgs {
   PagedView c;
@@ -68,7 +69,7 @@ struct EvictArgs {
   long long ldwo;
   int* lens_out;           // [batch]
 };
-cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a);
+cudaError_t launch_evict_paged(const Launch& L, const EvictArgs& a, int n_sm);
 // What ms_op_evict_paged says to these sizes; for callers that allocate the outputs.
 ms_status check_evict_sizes(const ms_paged_kv& kv, int64_t ldw, int dst_pages, int keep, int first, int recent, int64_t ldw_out);
 
@@ -84,6 +85,6 @@ struct VerifyArgs {
   int* accepted;
   int* out;                // [batch][max_draft + 1]
 };
-cudaError_t launch_verify_draft(const Launch& L, const VerifyArgs& a);
+cudaError_t launch_verify_draft(const Launch& L, const VerifyArgs& a, int n_sm);
 
 }  // namespace ms
