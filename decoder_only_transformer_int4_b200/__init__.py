@@ -357,7 +357,8 @@ def attn_paged(kv: PagedKV, q: torch.Tensor, row_start: torch.Tensor, max_rows: 
                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of the newest rows q [rows, heads, dim] (at most max_rows of a sequence) over the paged cache
     (ms_op_attn_paged); scale defaults to dim ** -0.5.  weights fp32 [batch, kv_heads, >= capacity] grows by each
-    position's probabilities.  workspace: uint8, attn_paged_workspace bytes; one is allocated where None."""
+    position's probabilities.  workspace: uint8, attn_paged_workspace bytes (with weights it holds a score for every row and
+    place of the tables); one is allocated where None."""
     r = _paged.attn(kv._h, q, row_start, max_rows, scale, weights, out, workspace)
     if r[0]:
         _check(r[0], "ms_op_attn_paged")

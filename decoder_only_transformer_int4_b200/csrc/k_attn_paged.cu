@@ -6,17 +6,17 @@
 // heads of group g.
 //
 // Bound: HBM, every K and V row of a sequence is read once for all heads of its group and all newest
-// rows, up to 32 at a time (2 T Hk hd elements).  One cache of 131071 positions (8 kv heads of 64, fp16) takes 48 us with
+// rows, up to 32 at a time, 16 with an fp32 cache (2 T Hk hd elements a pass).  One cache of 131071 positions (8 kv heads of 64, fp16) takes 48 us with
 // the join, 5.5 TB/s; 16 ragged sequences of up to 16411 (8 heads of 128, bf16) 98 us at one row each (6.1 TB/s)
-// and 115 us at up to six, where a tile of 24 rows costs about as many issue slots as the memory leaves.  64 sequences
-// of 505 to 1024 take 17.5 us (19.4 with weights) for 52 MB: 4.5 us until the first tile is there, then seven tiles
-// a CTA, then the join.
+// and 115 us at up to six (5.7 TB/s while the first kernel runs), where a tile of 24 rows costs about as many issue slots as the
+// memory leaves.  64 sequences of 505 to 1024 take 17.5 us (19.8 with weights) for 52 MB: 4.5 us until the first tile is
+// there, then seven tiles a CTA, then the join.
 //
 // The products stay on warp-level MMAs: S^T = K Q^T and O^T = V^T P^T, sixteen cached positions (or elements
 // of a head) on the M side, rows in tiles of 8 on the N side, so that the 3 or 4 rows of a decoding group pad to 8.
-// tcgen05 was built and measured for more than 16 rows (128 positions a tile, one to a TMEM lane): 200 us against 115 on
-// the case above, 100 against 83 at 56 rows.  Its products are short; what a tile costs is its copies through the
-// load-store path and the softmax of its rows, which eight warps there do in step and twelve here do each in its own time.
+// A tcgen05 variant for more than 16 rows (128 positions a tile, one to a TMEM lane, sums in TMEM) was built and left out: 200 us
+// against 115 on the case above, 100 against 83 at 56 rows.  It moved its tiles with cp.async through the load-store path, a third
+// of its time a tile, and one group of eight softmax warps worked in step; with TMA copies it has not been tried.
 //
 // Split.  The positions of all (sequence, kv head, row tile) units are cut into tiles of 64 and laid
 // end to end; every resident CTA takes an equal run of tiles, whatever the lengths.  A run crosses
@@ -81,7 +81,7 @@ struct Kargs {
   void* out;
   long long ldq, ldo;
   const int* row_start;
-  int rows, max_rows, H, hpg, rb;   // rb: the most row tiles a (sequence, kv head) may have
+  int rows, max_rows, hpg, rb;      // rb: the most row tiles a (sequence, kv head) may have
   float scale2;                     // scale * log2(e)
   float* part;                      // [CTAs][2][R][hd] unscaled sums of cut units
   float2* ml;                       // [CTAs][2][R] their (max, sum)
@@ -109,7 +109,7 @@ struct Shape {
   static constexpr int R = 8 * NB;
   static constexpr int kRowBytes = HD * sizeof(KT);
   static constexpr int kStageBytes = 2 * kStep * kRowBytes;      // K then V of one warp's step
-  // 16 KB (fp32, 128 elements): one stage and three CTAs an SM instead of two stages and one CTA
+  // 16 KB (fp32, 128 elements): one stage and two CTAs an SM instead of two stages and one CTA
   // (67 sequences of 20 heads on 5: 37 us, 48 with two stages)
   static constexpr int kStages = kStageBytes <= 4096 ? 3 : kStageBytes <= 8192 ? 2 : 1;
   static constexpr int kQBytes = R * HD * ((kF32 || Q32) ? 4 : 2);   // Q32 on halves: hi and lo planes
@@ -1361,7 +1361,6 @@ cudaError_t attn_go(const Launch& L, const AttnPagedArgs& a, int n_sm, void* ws)
   k.row_start = a.row_start;
   k.rows = a.rows;
   k.max_rows = a.max_rows;
-  k.H = a.H;
   k.hpg = p.hpg;
   k.rb = p.rb;
   k.scale2 = a.scale * 1.44269504088896340736f;

@@ -76,7 +76,7 @@ __device__ __forceinline__ void pack(Pack<__nv_bfloat16, N>& p, const float (&y)
 // out once for all heads.  A thread then has the same two chunks of 16 bytes in every so-manyth head of its
 // token, so that its sines stay in registers (read from shared memory for each head, their bank conflicts and
 // loads held bf16 rows to half the bandwidth).  32767 rows of 40 heads of 64, fp32 to fp16: 98 us, 6.2 TB/s;
-// 4132 rows of 48 bf16 heads of 128: 21.8 us, 4.7 TB/s (the chain at the start shows); 64 rows: 3.1 us.
+// 4132 rows of 48 bf16 heads of 128: 20.2 us, 5.0 TB/s (the chain at the start shows); 64 rows: 3.1 us.
 // ---------------------------------------------------------------------------------
 namespace {
 constexpr int kRopeThreads = 256, kRopeTokens = 32;
@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_paged_kernel(Rope
     }
   } else {
     // odd strides, unaligned rows or half-layout pairs that do not fall on chunks: a thread moves
-    // the two elements of a pair (of two passing elements) at a time
+    // the two elements of a pair (of two passing elements) at a time (the sizes above with pairs of 30 elements: 205 and 82 us,
+    // floors 93 and 17)
     rope_tokens(a, t0, nt, cs, info);
     const int per = hd / 2, items = heads * per;
     for (int it = tid; it < nt * items; it += kRopeThreads) {
@@ -370,7 +371,7 @@ cudaError_t launch_rope_append_paged(const Launch& L, const RopeArgs& a, int q_e
 //
 // Bound: HBM, 2 x kept rows read and written (10.7 and 20.8 us at 64 x 4 x 512 rows of 128 bytes and
 // 4 x 8 x 4099 of 256); the select is latency: a digit takes 0.6 us in one CTA, 2 to 2.4 in a cluster (its barrier 0.9, the sum of
-// its histograms 0.5).  20.2 and 38.8 us; all four digits 20.5 and 41.2; one CTA per (sequence, kv head) with a second
+// its histograms 0.5).  20.9 and 39 us; all four digits 20.5 and 41.2; one CTA per (sequence, kv head) with a second
 // kernel for the rows 26.9 and 78.4, of that the select 14 and 56.  Moving the rows that stay in any case while the barriers are
 // waited for did not pay (21.8 and 44.5): their loads delay the select's.
 // ---------------------------------------------------------------------------------
@@ -556,14 +557,13 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_paged_kernel(EvictArgs a,
       __syncthreads();
       prefix = (prefix << 8) | (unsigned)picked[pass][0];
       left = picked[pass][1];
-      const int shifted = shift;
       if (pass == 3) {
         key = prefix;
         equal = left;
       } else if (picked[pass][2] <= kEvFew) {
         // every CTA gets them all, in any order
         each([&](int, unsigned u) {
-          if ((u >> shifted) == prefix) {
+          if ((u >> shift) == prefix) {
             const int at = atomicAdd(cluster.map_shared_rank(&few_count, 0), 1);
             for (int r = 0; r < C; ++r) cluster.map_shared_rank(few, r)[at] = u;
           }

@@ -429,7 +429,8 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
  * 2^-35 of its row's largest is lost of a probability, so that one below that may count as 0; with the other types
  * they keep 16 bits (bf16) or 21 and more, however far one position leads the others.  The
  * result of a sequence does not depend on timing, but its rounding on how the batch's work is split.
- * workspace: ms_op_attn_paged_workspace bytes (0 for arguments that the call refuses), 256-byte
+ * workspace: ms_op_attn_paged_workspace bytes (some MB; with weights also 4 * batch * n_heads * max_rows * max_pages
+ * page_size for the scores, whatever the lengths; 0 for arguments that the call refuses), 256-byte
  * aligned, holding nothing before or after; calls that may overlap on the GPU need their own, and their own weights.
  * rows <= 2^30, max_pages * page_size < 2^30, batch * n_heads * max_rows * max_pages * page_size <= 2^36. */
 size_t ms_op_attn_paged_workspace(const ms_paged_kv* kv, int q_elem, int n_heads, int max_rows, int with_weights);
