@@ -417,8 +417,9 @@ ms_status ms_op_rope_append_paged(const ms_paged_kv* kv, const void* q, int64_t 
  * h / (n_heads / n_kv_heads):
  *     out = sum_t p_t v_t,   p = softmax_t(scale * q . k_t).
  * A row that sees no position (T = 0, or n > T) gives 0.  What lies behind a sequence's end, or a row's last visible
- * position, never enters, whatever the memory holds; a k or v that is not finite makes the rows that see it so
- * (fp32: of magnitude below 2^127).  n <= max_rows (1 .. 64): one row is decoding,
+ * position, never enters, whatever the memory holds; a k or v that is not finite makes the rows that see it so.
+ * Finite ones hold where fp32 does: |q k| sums below 2^127, fp32 k below 2^127, fp32 and bf16 v below 2^92 in magnitude (sums of v
+ * are divided at the end).  n <= max_rows (1 .. 64): one row is decoding,
  * several are drafts.  out may be q (with ldo = ldq), else they must not
  * overlap.  q and out [rows][n_heads][head_dim] of q_elem at strides ldq, ldo; rows behind
  * row_start[batch] are left as they were.
@@ -445,6 +446,7 @@ ms_status ms_op_attn_paged(const ms_paged_kv* kv, const void* q, int64_t ldq, in
  * 0, 1, .. of the pages that dst_table (int32 [batch][dst_pages]) gives the sequence, of the same page
  * arrays; a row for which it has no page (dst_pages need only hold what the longest sequence keeps) is left out and flagged.  The pages of dst_table must not be read by
  * this call's sequences (kv->table), except that a sequence which keeps all may keep its pages: the same entries in both.
+ * No page that a sequence moves to may stand in dst_table twice.
  * weights fp32 [batch][n_kv_heads][ldw] -> weights_out [batch][n_kv_heads][ldw_out], the kept positions'
  * weights in the new order and 0 behind; weights_out may be weights (with ldw_out = ldw), else
  * they must not overlap.  ldw >= max_pages * page_size, ldw_out >= min(keep, max_pages *

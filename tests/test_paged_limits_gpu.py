@@ -126,6 +126,18 @@ def test_attention_where_the_heaviest_position_holds_nothing(kq, kkv, hd, T, nat
     tol = R.half_step(kq) * np.abs(ref) + A * (3 * U * spread + 8 * U + (2.0 ** -17 if kkv == "bf16" else 2.0 ** -21) + 2 * T * U)[..., None]
     assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / np.maximum(A, 1e-300)).max()
 
+@pytest.mark.parametrize("kq,kkv,v", [("bf16", "bf16", 2.0 ** 91), ("f32", "f32", 2.0 ** 91), ("f32", "f16", 65504.0), ("f16", "f16", 65504.0)])
+def test_attention_of_the_largest_values(kq, kkv, v):
+    # the sums over 3000 positions, before they are divided, stay finite (an fp16 result may round up to infinity)
+    T = 3000
+    pages = R.Pages([T], 1, 64, 64, kkv, seed=461)
+    pages.v = torch.where(torch.isnan(pages.v), pages.v, torch.full_like(pages.v, v))
+    q = torch.ones((1, 4, 64)).to(R.TYPES[kq])
+    got = R.f64(ms.attn_paged(pages.cuda(ms), q.cuda(), R.starts([1]).cuda(), 1))
+    # all v are the same: the two sums over T positions, exp2 twice, the pairs; then one rounding
+    rel = R.half_step(kq) + 2 * T * U + 8 * U + (2.0 ** -17 if kkv == "bf16" else 2.0 ** -21)
+    assert np.all(np.isfinite(got) | (kq == "f16")) and np.all(np.abs(np.minimum(got, v) - v) <= rel * v)
+
 
 # ---- verification ---------------------------------------------------------------------------------
 
