@@ -9,7 +9,7 @@
 // rows, up to 32 at a time, 16 with an fp32 cache (2 T Hk hd elements a pass).  One cache of 131071 positions (8 kv heads of 64, fp16) takes 48 us with
 // the join, 5.5 TB/s; 16 ragged sequences of up to 16411 (8 heads of 128, bf16) 98 us at one row each (6.1 TB/s)
 // and 115 us at up to six (5.7 TB/s while the first kernel runs), where a tile of 24 rows costs about as many issue slots as the
-// memory leaves.  64 sequences of 505 to 1024 take 17.5 us (19.8 with weights) for 52 MB: 4.5 us until the first tile is
+// memory leaves.  64 sequences of 505 to 1024 take 18.0 us (19.8 with weights) for 52 MB: 4.5 us until the first tile is
 // there, then seven tiles a CTA, then the join.
 //
 // The products stay on warp-level MMAs: S^T = K Q^T and O^T = V^T P^T, sixteen cached positions (or elements
@@ -24,7 +24,7 @@
 // for the piece that begins a CTA's run and one for the piece that ends it, which attn_finish_kernel adds.
 // Nothing waits for another CTA, no counter has to be cleared, and the order of every sum is fixed.
 // A call whose units all fit the GPU as clusters with at most two tiles to a CTA (1024 positions) joins over
-// distributed shared memory instead, in one launch: one fp32 stream of 577 positions 6.9 us, 9.5 in two kernels; with eight
+// distributed shared memory instead, in one launch: one fp32 stream of 577 positions 6.7 us, 9.5 in two kernels; with eight
 // tiles to a CTA (4000 positions) the cluster's 14.1 us lose to 8.8.
 //
 // Inside a CTA each warp takes its own 16 positions of every tile and streams them with cp.async
